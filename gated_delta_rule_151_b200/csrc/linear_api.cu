@@ -1,0 +1,325 @@
+// C ABI of linear attention with a decay for each head: argument checks, the
+// plan (how sequences are cut into segments), workspace layout and launches.
+#include <algorithm>
+#include <cstdint>
+
+#include "api_common.h"
+#include "common.cuh"
+#include "linear_common.cuh"
+
+namespace gdr {
+namespace {
+
+using api::apart;
+using api::given16;
+using api::head_dim;
+using api::io_type;
+using api::maybe16;
+using api::Range;
+
+constexpr size_t kHeader = 256;
+constexpr int kSMs = 148;
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct Plan {
+    int seg_tokens, slots, inner;
+};
+
+// Cost of a 64-token block of one head in the output and the state pass, and
+// what a CTA and the pass between segments cost beside, in microseconds, with
+// `at_once` CTAs resident on the GPU.
+struct Costs {
+    int at_once;
+    double block, state, cta, join;
+};
+
+Costs costs_of(int d_b, int d_v) {
+    return Costs{kSMs * 2, 0.06 * d_b + 2.0, 0.04 * d_b + 2.0, 3.0, 4.0};
+}
+
+// Equal lengths: the segment length whose passes end first by the costs above,
+// one wave of segments after another.  Packed lengths are not known here:
+// about two segments for every place on the GPU bound what one long sequence
+// can cost, and shorter sequences stay whole.
+Plan make_plan(int N, int total_T, int H, int d_b, int d_v, bool equal) {
+    const Costs c = costs_of(d_b, d_v);
+    Plan p;
+    if (!equal) {
+        const int64_t blocks = ((int64_t)total_T + kScanBlock - 1) / kScanBlock;
+        const int64_t per = std::max<int64_t>(8, (blocks * H + 2 * c.at_once - 1) / (2 * c.at_once));
+        p.seg_tokens = (int)std::min<int64_t>(per, INT32_MAX / kScanBlock) * kScanBlock;
+        p.inner = total_T / p.seg_tokens;
+        p.slots = N + p.inner;
+        return p;
+    }
+    const int len = total_T / N;
+    const int64_t blocks = std::max(1, (len + kScanBlock - 1) / kScanBlock), chains = (int64_t)N * H;
+    auto waves = [&](int64_t items) { return (double)((items + c.at_once - 1) / c.at_once); };
+    int64_t best = blocks;
+    double least = waves(chains) * (blocks * c.block + c.cta);
+    for (int64_t segs = 2; segs <= std::min<int64_t>(blocks, 2 * c.at_once); ++segs) {
+        const int64_t per = (blocks + segs - 1) / segs, n = (blocks + per - 1) / per;
+        const double t = waves(chains * (n - 1)) * (per * c.state + c.cta) +
+                         waves(chains * n) * (per * c.block + c.cta) + c.join;
+        if (t < least) {
+            least = t;
+            best = per;
+        }
+    }
+    const int64_t n = (blocks + best - 1) / best;
+    p.seg_tokens = (int)best * kScanBlock;
+    p.slots = (int)(N * n);
+    p.inner = (int)(N * (n - 1));
+    return p;
+}
+
+// Workspace of one call: header, status words of every pass, a copy of the
+// incoming state, the states between segments, fp32 partial gradients.
+struct Layout {
+    size_t status, copy, seg, part, total;
+    uint32_t words;
+};
+
+Layout make_layout(const Plan &p, int N, int total_T, int H_qk, int H, int d_k, int d_v,
+                   bool backward) {
+    Layout l;
+    const size_t state = (size_t)H * d_k * d_v * 4;
+    l.words = (uint32_t)((size_t)(p.slots + p.inner) * H * (backward ? 3 : 1));
+    l.status = kHeader;
+    l.copy = l.status + up256((size_t)l.words * 4);
+    l.seg = l.copy + (p.inner > 0 && !backward ? up256(N * state) : 0);
+    l.part = l.seg + up256(p.inner * state);
+    l.total = l.part + (backward && H != H_qk ? up256((size_t)total_T * H * d_k * 4) : 0);
+    return l;
+}
+
+size_t workspace_bytes(int N, int total_T, int H_qk, int H, int d_k, int d_v, bool backward) {
+    if (N == 0 || total_T == 0) return 0;
+    size_t most = 0;
+    for (int equal = 0; equal < 2; ++equal) {
+        if (equal && total_T % N != 0) continue;
+        const Plan p = make_plan(N, total_T, H, d_k, d_v, equal != 0);
+        most = std::max(most, make_layout(p, N, total_T, H_qk, H, d_k, d_v, backward).total);
+    }
+    return most;
+}
+
+struct Call {
+    const int32_t *cu;
+    const float *decay;
+    int N, total_T, H;
+    Plan plan;
+    Layout lay;
+    uint8_t *ws;
+    bool bf16;
+    cudaStream_t stream;
+    uint32_t used;   // status words handed out
+
+    cudaError_t scan(const void *a, int HA, const void *b, int HB, const void *v, int HV, int d_b,
+                     int d_v, const float *s_in, bool turned, float *s_out, void *out, bool out_f32,
+                     bool reverse) {
+        ScanArgs p;
+        p.a = a; p.b = b; p.v = v;
+        p.out = out;
+        p.decay = decay;
+        p.s_in = s_in;
+        p.s_out = s_out;
+        p.seg = reinterpret_cast<float *>(ws + lay.seg);
+        p.header = reinterpret_cast<uint32_t *>(ws);
+        p.status = reinterpret_cast<uint32_t *>(ws + lay.status) + used;
+        p.status_words = 0;
+        p.cu = cu;
+        p.N = N; p.total_T = total_T; p.H = H;
+        p.HA = HA; p.HB = HB; p.HV = HV;
+        p.seg_tokens = plan.seg_tokens;
+        p.slots = plan.slots;
+        p.inner = plan.inner;
+        p.turned = turned;
+        cudaError_t e = cudaSuccess;
+        if (plan.inner > 0) {
+            e = pass(p, d_b, d_v, reverse, true, out_f32);
+            if (e == cudaSuccess) e = launch_scan_join(p, d_b * d_v, reverse, stream);
+            p.status += (size_t)plan.inner * H;
+        }
+        if (e == cudaSuccess) e = pass(p, d_b, d_v, reverse, false, out_f32);
+        used += (uint32_t)(plan.slots + plan.inner) * H;
+        return e;
+    }
+
+    cudaError_t pass(const ScanArgs &p, int d_b, int d_v, bool reverse, bool states, bool out_f32) {
+        return launch_scan_simt(p, d_b, d_v, reverse, states, bf16, out_f32, stream);
+    }
+};
+
+// Shapes both directions share; GDR_OK with *todo = false when nothing is to be run.
+gdr_status_t check_shape(int32_t num_seqs, int32_t total_T, int32_t H_qk, int32_t H, int32_t d_k,
+                         int32_t d_v, gdr_dtype_t io_dtype, bool equal) {
+    if (num_seqs < 0 || total_T < 0 || H < 1 || H_qk < 1 || H % H_qk != 0) return GDR_ERR_INVALID_ARG;
+    if (!head_dim(d_k) || !head_dim(d_v) || !io_type(io_dtype)) return GDR_ERR_INVALID_ARG;
+    if (num_seqs == 0 && total_T != 0) return GDR_ERR_INVALID_ARG;
+    if (equal && num_seqs > 0 && total_T % num_seqs != 0) return GDR_ERR_INVALID_ARG;
+    // token, grid and status indices are 32-bit
+    if ((int64_t)total_T * H > INT32_MAX || (int64_t)num_seqs * H > INT32_MAX / 8)
+        return GDR_ERR_INVALID_ARG;
+    return GDR_OK;
+}
+
+cudaError_t pass_state(float *dst, const float *src, size_t bytes, cudaStream_t s) {
+    if (dst == nullptr || dst == src || bytes == 0) return cudaSuccess;
+    if (src == nullptr) return cudaMemsetAsync(dst, 0, bytes, s);
+    return cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToDevice, s);
+}
+
+gdr_status_t status_of(cudaError_t e) { return e == cudaSuccess ? GDR_OK : GDR_ERR_CUDA; }
+
+}  // namespace
+}  // namespace gdr
+
+using namespace gdr;
+
+extern "C" {
+
+gdr_status_t gdr_linear_workspace_size(int32_t num_seqs, int32_t total_T, int32_t H_qk, int32_t H,
+                                       int32_t d_k, int32_t d_v, gdr_dtype_t io_dtype,
+                                       int32_t backward, size_t *bytes) {
+    if (bytes == nullptr) return GDR_ERR_INVALID_ARG;
+    const gdr_status_t st = check_shape(num_seqs, total_T, H_qk, H, d_k, d_v, io_dtype, false);
+    if (st != GDR_OK) return st;
+    *bytes = workspace_bytes(num_seqs, total_T, H_qk, H, d_k, d_v, backward != 0);
+    return GDR_OK;
+}
+
+gdr_status_t gdr_linear_prefill(const void *q, const void *k, const void *v, const float *decay,
+                                const float *initial_state, const int32_t *cu_seqlens,
+                                int32_t num_seqs, int32_t total_T, int32_t H_qk, int32_t H,
+                                int32_t d_k, int32_t d_v, gdr_dtype_t io_dtype, void *o,
+                                float *final_state, void *workspace, size_t workspace_bytes,
+                                void *stream) {
+    const bool equal = cu_seqlens == nullptr;
+    gdr_status_t st = check_shape(num_seqs, total_T, H_qk, H, d_k, d_v, io_dtype, equal);
+    if (st != GDR_OK) return st;
+    if (!maybe16(initial_state) || !maybe16(final_state) || !api::aligned(cu_seqlens, 4))
+        return GDR_ERR_INVALID_ARG;
+    if (num_seqs == 0) return GDR_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t state = (size_t)num_seqs * H * d_k * d_v * 4;
+    const size_t e = io_dtype == GDR_BF16 ? 2 : 4, T = (size_t)total_T;
+    if (total_T > 0 && (!given16(q) || !given16(k) || !given16(v) || !given16(o) || decay == nullptr ||
+                        !api::aligned(decay, 4)))
+        return GDR_ERR_INVALID_ARG;
+    const Plan plan = total_T > 0 ? make_plan(num_seqs, total_T, H, d_k, d_v, equal) : Plan{kScanBlock, 0, 0};
+    const Layout lay = make_layout(plan, num_seqs, total_T, H_qk, H, d_k, d_v, false);
+    const size_t need = total_T > 0 ? lay.total : 0;
+    if (need > 0 && (!given16(workspace) || workspace_bytes < need)) return GDR_ERR_WORKSPACE;
+    const Range in[] = {{q, T * H_qk * d_k * e}, {k, T * H_qk * d_k * e}, {v, T * H * d_v * e},
+                        {decay, (size_t)H * 4},
+                        {initial_state == final_state ? nullptr : initial_state, state},
+                        {cu_seqlens, equal ? 0 : ((size_t)num_seqs + 1) * 4}};
+    const Range out[] = {{o, T * H * d_v * e}, {final_state, state}, {workspace, need}};
+    if (!apart(in, out)) return GDR_ERR_INVALID_ARG;
+    if (total_T == 0) return status_of(pass_state(final_state, initial_state, state, s));
+
+    Call c{cu_seqlens, decay, num_seqs, total_T, H, plan, lay, static_cast<uint8_t *>(workspace),
+           io_dtype == GDR_BF16, s, 0};
+    // in place and in segments: the last segment of a sequence may end before its
+    // first one has read the incoming state, which therefore moves aside
+    if (initial_state != nullptr && initial_state == final_state && plan.inner > 0) {
+        float *copy = reinterpret_cast<float *>(c.ws + lay.copy);
+        if (pass_state(copy, initial_state, state, s) != cudaSuccess) return GDR_ERR_CUDA;
+        initial_state = copy;
+    }
+    return status_of(c.scan(q, H_qk, k, H_qk, v, H, d_k, d_v, initial_state, false, final_state, o,
+                            false, false));
+}
+
+gdr_status_t gdr_linear_check_workspace(const void *workspace, size_t workspace_bytes, void *stream) {
+    if (!given16(workspace) || workspace_bytes < kHeader) return GDR_ERR_WORKSPACE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const uint8_t *ws = static_cast<const uint8_t *>(workspace);
+    uint32_t words = 0;
+    if (cudaMemcpyAsync(&words, ws, 4, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return GDR_ERR_CUDA;
+    if ((size_t)words > (workspace_bytes - kHeader) / 4) return GDR_ERR_WORKSPACE;
+    uint32_t any = 0, part[1024];
+    for (size_t at = 0; at < words; at += 1024) {
+        const size_t n = std::min<size_t>(1024, words - at);
+        if (cudaMemcpyAsync(part, ws + kHeader + at * 4, n * 4, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+            cudaStreamSynchronize(s) != cudaSuccess)
+            return GDR_ERR_CUDA;
+        for (size_t i = 0; i < n; ++i) any |= part[i];
+    }
+    return any == 0 ? GDR_OK : GDR_ERR_DEVICE_TIMEOUT;
+}
+
+gdr_status_t gdr_linear_decode(const void *q, const void *k, const void *v, const float *decay,
+                               float *state, int32_t N, int32_t H_qk, int32_t H, int32_t d_k,
+                               int32_t d_v, gdr_dtype_t io_dtype, void *o, void *stream) {
+    if (N < 0 || H < 1 || H_qk < 1 || H % H_qk != 0) return GDR_ERR_INVALID_ARG;
+    if (!head_dim(d_k) || !head_dim(d_v) || !io_type(io_dtype)) return GDR_ERR_INVALID_ARG;
+    if ((int64_t)N * H > INT32_MAX) return GDR_ERR_INVALID_ARG;
+    if (N == 0) return GDR_OK;
+    if (!given16(q) || !given16(k) || !given16(v) || !given16(state) || !given16(o) ||
+        decay == nullptr || !api::aligned(decay, 4))
+        return GDR_ERR_INVALID_ARG;
+    const size_t e = io_dtype == GDR_BF16 ? 2 : 4, n = (size_t)N;
+    const Range in[] = {{q, n * H_qk * d_k * e}, {k, n * H_qk * d_k * e}, {v, n * H * d_v * e},
+                        {decay, (size_t)H * 4}};
+    const Range out[] = {{o, n * H * d_v * e}, {state, n * H * d_k * d_v * 4}};
+    if (!apart(in, out)) return GDR_ERR_INVALID_ARG;
+    return status_of(launch_linear_decode(q, k, v, decay, state, N, H_qk, H, d_k, d_v,
+                                          io_dtype == GDR_BF16, o, static_cast<cudaStream_t>(stream)));
+}
+
+gdr_status_t gdr_linear_backward(const void *q, const void *k, const void *v, const float *decay,
+                                 const float *initial_state, const int32_t *cu_seqlens,
+                                 int32_t num_seqs, int32_t total_T, int32_t H_qk, int32_t H,
+                                 int32_t d_k, int32_t d_v, gdr_dtype_t io_dtype, const void *d_o,
+                                 const float *d_final_state, void *dq, void *dk, void *dv,
+                                 float *d_initial_state, void *workspace, size_t workspace_bytes,
+                                 void *stream) {
+    const bool equal = cu_seqlens == nullptr;
+    gdr_status_t st = check_shape(num_seqs, total_T, H_qk, H, d_k, d_v, io_dtype, equal);
+    if (st != GDR_OK) return st;
+    if (!maybe16(initial_state) || !maybe16(d_final_state) || !maybe16(d_initial_state) ||
+        !api::aligned(cu_seqlens, 4))
+        return GDR_ERR_INVALID_ARG;
+    if (num_seqs == 0) return GDR_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t state = (size_t)num_seqs * H * d_k * d_v * 4;
+    const size_t e = io_dtype == GDR_BF16 ? 2 : 4, T = (size_t)total_T;
+    if (total_T > 0 && (!given16(q) || !given16(k) || !given16(v) || !given16(d_o) || !given16(dq) ||
+                        !given16(dk) || !given16(dv) || decay == nullptr || !api::aligned(decay, 4)))
+        return GDR_ERR_INVALID_ARG;
+    const Plan plan = total_T > 0 ? make_plan(num_seqs, total_T, H, d_k, d_v, equal) : Plan{kScanBlock, 0, 0};
+    const Layout lay = make_layout(plan, num_seqs, total_T, H_qk, H, d_k, d_v, true);
+    const size_t need = total_T > 0 ? lay.total : 0;
+    if (need > 0 && (!given16(workspace) || workspace_bytes < need)) return GDR_ERR_WORKSPACE;
+    const size_t nq = T * H_qk * d_k * e, nv = T * H * d_v * e;
+    const Range in[] = {{q, nq}, {k, nq}, {v, nv}, {decay, (size_t)H * 4}, {initial_state, state},
+                        {d_o, nv}, {d_final_state, state},
+                        {cu_seqlens, equal ? 0 : ((size_t)num_seqs + 1) * 4}};
+    const Range out[] = {{dq, nq}, {dk, nq}, {dv, nv}, {d_initial_state, state}, {workspace, need}};
+    if (!apart(in, out)) return GDR_ERR_INVALID_ARG;
+    if (total_T == 0) return status_of(pass_state(d_initial_state, d_final_state, state, s));
+
+    Call c{cu_seqlens, decay, num_seqs, total_T, H, plan, lay, static_cast<uint8_t *>(workspace),
+           io_dtype == GDR_BF16, s, 0};
+    // heads that share a query/key head: each one's dq and dk in fp32, then their sum
+    const int group = H / H_qk;
+    float *part = reinterpret_cast<float *>(c.ws + lay.part);
+    cudaError_t r = c.scan(d_o, H, v, H, k, H_qk, d_v, d_k, initial_state, true, nullptr,
+                           group > 1 ? part : dq, group > 1, false);
+    if (r == cudaSuccess && group > 1) r = launch_group_sum(part, total_T, H_qk, group, d_k, c.bf16, dq, s);
+    if (r == cudaSuccess)
+        r = c.scan(v, H, d_o, H, q, H_qk, d_v, d_k, d_final_state, true, nullptr,
+                   group > 1 ? part : dk, group > 1, true);
+    if (r == cudaSuccess && group > 1) r = launch_group_sum(part, total_T, H_qk, group, d_k, c.bf16, dk, s);
+    if (r == cudaSuccess)
+        r = c.scan(k, H_qk, q, H_qk, d_o, H, d_k, d_v, d_final_state, false, d_initial_state, dv,
+                   false, true);
+    return status_of(r);
+}
+
+}  // extern "C"

@@ -33,6 +33,9 @@ GDR_PATH_TCGEN05 = 1
 GDR_PATH_TCGEN05_SPLIT = 2
 GDR_PROLOGUE_SILU = 1
 GDR_PROLOGUE_NORMALIZE_QK = 2
+GDR_ACT_NONE = 0
+GDR_ACT_SILU = 1
+GDR_ACT_SIGMOID = 2
 
 # Every symbol include/gdr.h declares.
 EXPORTED = ("gdr_status_string", "gdr_prefill_workspace_size", "gdr_prefill_path",
@@ -40,7 +43,10 @@ EXPORTED = ("gdr_status_string", "gdr_prefill_workspace_size", "gdr_prefill_path
             "gdr_prefill_chunked_noalloc", "gdr_prefill_chunked_gqa", "gdr_decode_step_gqa",
             "gdr_decode_multi", "gdr_prefill_plan", "gdr_prologue", "gdr_backward",
             "gdr_backward_workspace_size", "gdr_prefill_noalloc_check",
-            "gdr_test_noalloc_wait_timeout", "gdr_prefill_fused")
+            "gdr_test_noalloc_wait_timeout", "gdr_prefill_fused", "gdr_linear_workspace_size",
+            "gdr_linear_prefill", "gdr_linear_decode", "gdr_linear_backward",
+            "gdr_linear_check_workspace", "gdr_norm_gate", "gdr_norm_gate_workspace_size",
+            "gdr_norm_gate_backward")
 
 
 class GdrError(RuntimeError):
@@ -106,6 +112,24 @@ def load_library():
         lib.gdr_backward_workspace_size.restype = ST
         lib.gdr_backward.argtypes = [P] * 7 + [I32] * 6 + [ST, ST] + [P] * 9 + [SZ, P]
         lib.gdr_backward.restype = ST
+        I64, F32 = ctypes.c_int64, ctypes.c_float
+        lib.gdr_linear_workspace_size.argtypes = [I32] * 6 + [ST, I32, ctypes.POINTER(SZ)]
+        lib.gdr_linear_workspace_size.restype = ST
+        lib.gdr_linear_prefill.argtypes = [P] * 6 + [I32] * 6 + [ST, P, P, P, SZ, P]
+        lib.gdr_linear_prefill.restype = ST
+        lib.gdr_linear_decode.argtypes = [P] * 5 + [I32] * 5 + [ST, P, P]
+        lib.gdr_linear_decode.restype = ST
+        lib.gdr_linear_backward.argtypes = [P] * 6 + [I32] * 6 + [ST] + [P] * 7 + [SZ, P]
+        lib.gdr_linear_backward.restype = ST
+        lib.gdr_linear_check_workspace.argtypes = [P, SZ, P]
+        lib.gdr_linear_check_workspace.restype = ST
+        lib.gdr_norm_gate.argtypes = [P] * 5 + [I64, I32, F32, F32, ST, ST, P, P, P]
+        lib.gdr_norm_gate.restype = ST
+        lib.gdr_norm_gate_workspace_size.argtypes = [I64, I32, ctypes.POINTER(SZ)]
+        lib.gdr_norm_gate_workspace_size.restype = ST
+        lib.gdr_norm_gate_backward.argtypes = ([P] * 5 + [I64, I32, F32, F32, ST, ST] + [P] * 8 +
+                                               [SZ, P])
+        lib.gdr_norm_gate_backward.restype = ST
         _lib = lib
         return lib
 
@@ -525,3 +549,278 @@ def gdr_backward(q, k, v, g, beta, initial_state=None, cu_seqlens=None, *, d_o,
         _stream_ptr(stream))
     _check(st, "gdr_backward")
     return dq, dk_, dv_, dg, db, dh0
+
+
+# ---- linear attention with a decay for each head, and the norms around a block ----
+#
+# These calls run on the device of their first argument, whichever device is
+# current, and allocate what the caller does not give under the stream they run
+# on, so that the memory is not handed out again while a kernel still uses it.
+
+_ACTIVATIONS = {"none": GDR_ACT_NONE, "silu": GDR_ACT_SILU, "sigmoid": GDR_ACT_SIGMOID}
+
+
+class _On:
+    """Makes ``device`` and ``stream`` current for a call; ``ptr`` is the stream's handle."""
+
+    def __init__(self, device, stream):
+        self._where, self._device = device, None
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self._device = torch.cuda.device(device)
+        self._given, self._stream = stream, None
+
+    def __enter__(self):
+        given = self._given
+        if given is not None and not isinstance(given, int) and given.device != self._where:
+            raise ValueError(f"stream is on {given.device}, the tensors on {self._where}")
+        if self._device is not None:
+            self._device.__enter__()
+        if given is None:
+            given = torch.cuda.current_stream()
+        else:
+            if isinstance(given, int):
+                given = torch.cuda.ExternalStream(given)
+            self._stream = torch.cuda.stream(given)
+            self._stream.__enter__()
+        self.ptr = ctypes.c_void_p(given.cuda_stream)
+        return self
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            self._stream.__exit__(*exc)
+        if self._device is not None:
+            self._device.__exit__(*exc)
+
+
+def _given(t, name, shape, dtype, device):
+    """One tensor argument: on the device, contiguous, of this type and shape."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _scratch(workspace, need, device):
+    """(pointer, bytes) of the caller's workspace or of a new one, and what keeps it alive."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _linear_args(q, k, v, decay, cu_seqlens, num_seqs):
+    """Checks what the linear-attention calls share; returns their sizes."""
+    _need(q, "q", ndim=3)
+    _need(v, "v", q.dtype, 3)
+    T, Hqk, dk = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    dev = q.device
+    _given(k, "k", (T, Hqk, dk), q.dtype, dev)
+    _given(v, "v", (T, H, dv), q.dtype, dev)
+    _given(decay, "decay", (H,), torch.float32, dev)
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be [N + 1]")
+        N = cu_seqlens.numel() - 1
+        _given(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
+        if num_seqs is not None and int(num_seqs) != N:
+            raise ValueError(f"num_seqs is {num_seqs}, cu_seqlens has {N} sequences")
+    else:
+        N = 1 if num_seqs is None else int(num_seqs)
+    return T, Hqk, H, dk, dv, N, dev, q.dtype
+
+
+def gdr_linear_workspace_size(num_seqs, total_T, H_qk, H, d_k, d_v, io_dtype,
+                              backward=False) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().gdr_linear_workspace_size(num_seqs, total_T, H_qk, H, d_k, d_v, io_dtype,
+                                                    int(backward), ctypes.byref(n)),
+           "gdr_linear_workspace_size")
+    return int(n.value)
+
+
+def gdr_linear_prefill(q, k, v, decay, initial_state=None, cu_seqlens=None, *, num_seqs=None,
+                       o=None, final_state=None, output_final_state=True, workspace=None,
+                       stream=None):
+    """Linear attention with a decay for each head over whole prompts (see
+    include/gdr.h).  Returns (o, final_state).
+
+    q, k [T, H_qk, d_k], v [T, H, d_v] (bf16 or fp32; H_qk divides H); decay
+    [H] fp32, the log-decays; initial_state [N, H, d_v, d_k] fp32 or None;
+    cu_seqlens int32 [N + 1] on the device, or None with ``num_seqs`` equal
+    sequences (default 1).  ``final_state`` may be initial_state.
+    """
+    T, Hqk, H, dk, dv, N, dev, io = _linear_args(q, k, v, decay, cu_seqlens, num_seqs)
+    code = _io_code(io)
+    if initial_state is not None:
+        _given(initial_state, "initial_state", (N, H, dv, dk), torch.float32, dev)
+    if o is not None:
+        _given(o, "o", (T, H, dv), io, dev)
+    if final_state is not None:
+        _given(final_state, "final_state", (N, H, dv, dk), torch.float32, dev)
+    with _On(dev, stream) as on:
+        need = gdr_linear_workspace_size(N, T, Hqk, H, dk, dv, code)
+        if o is None:
+            o = torch.empty((T, H, dv), dtype=io, device=dev)
+        if final_state is None and output_final_state:
+            final_state = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev)
+        ws, ws_bytes, _keep = _scratch(workspace, need, dev)
+        st = load_library().gdr_linear_prefill(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(initial_state), _ptr(cu_seqlens), N, T,
+            Hqk, H, dk, dv, code, _ptr(o), _ptr(final_state), ws, ws_bytes, on.ptr)
+    _check(st, "gdr_linear_prefill")
+    return o, final_state
+
+
+def gdr_linear_check_workspace(workspace, stream=None):
+    """Raise GdrError(GDR_ERR_DEVICE_TIMEOUT) if a bounded device-side wait of
+    the call that used this workspace gave up (synchronises the stream)."""
+    with _On(workspace.device, stream) as on:
+        st = load_library().gdr_linear_check_workspace(
+            _ptr(workspace), workspace.numel() * workspace.element_size(), on.ptr)
+    _check(st, "gdr_linear_check_workspace")
+
+
+def gdr_linear_decode(q, k, v, decay, state, *, o=None, stream=None):
+    """One token per sequence (see include/gdr.h): state is updated in place.
+
+    q, k [N, H_qk, d_k], v [N, H, d_v] (bf16 or fp32); decay [H] fp32; state
+    [N, H, d_v, d_k] fp32.  Returns o [N, H, d_v].
+    """
+    N, Hqk, H, dk, dv, _, dev, io = _linear_args(q, k, v, decay, None, None)
+    _given(state, "state", (N, H, dv, dk), torch.float32, dev)
+    if o is not None:
+        _given(o, "o", (N, H, dv), io, dev)
+    with _On(dev, stream) as on:
+        if o is None:
+            o = torch.empty((N, H, dv), dtype=io, device=dev)
+        st = load_library().gdr_linear_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(state),
+                                              N, Hqk, H, dk, dv, _io_code(io), _ptr(o), on.ptr)
+    _check(st, "gdr_linear_decode")
+    return o
+
+
+def gdr_linear_backward(q, k, v, decay, initial_state=None, cu_seqlens=None, *, d_o,
+                        d_final_state=None, num_seqs=None, want_d_initial_state=True,
+                        workspace=None, stream=None):
+    """Gradient of <d_o, o> + <d_final_state, final_state> of
+    gdr_linear_prefill (see include/gdr.h).
+
+    d_o [T, H, d_v] in the io dtype; d_final_state [N, H, d_v, d_k] fp32 or
+    None.  Returns (dq, dk, dv, d_initial_state): the first three in the io
+    dtype, the last fp32 (None unless wanted).
+    """
+    T, Hqk, H, dk, dv, N, dev, io = _linear_args(q, k, v, decay, cu_seqlens, num_seqs)
+    code = _io_code(io)
+    _given(d_o, "d_o", (T, H, dv), io, dev)
+    for t, name in ((initial_state, "initial_state"), (d_final_state, "d_final_state")):
+        if t is not None:
+            _given(t, name, (N, H, dv, dk), torch.float32, dev)
+    with _On(dev, stream) as on:
+        need = gdr_linear_workspace_size(N, T, Hqk, H, dk, dv, code, True)
+        dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        dh0 = (torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev)
+               if want_d_initial_state else None)
+        ws, ws_bytes, _keep = _scratch(workspace, need, dev)
+        st = load_library().gdr_linear_backward(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(initial_state), _ptr(cu_seqlens), N, T,
+            Hqk, H, dk, dv, code, _ptr(d_o), _ptr(d_final_state), _ptr(dq), _ptr(dk_), _ptr(dv_),
+            _ptr(dh0), ws, ws_bytes, on.ptr)
+    _check(st, "gdr_linear_backward")
+    return dq, dk_, dv_, dh0
+
+
+def _norm_args(x, weight, gate, residual, next_weight, activation):
+    """Checks what the norm's two calls share; returns (rows, dim, device, dtype, activation)."""
+    _need(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dim")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, got {activation!r}")
+    dim, dev, shape = x.shape[-1], x.device, tuple(x.shape)
+    for t, name in ((gate, "gate"), (residual, "residual")):
+        if t is not None:
+            _given(t, name, shape, x.dtype, dev)
+    for t, name in ((weight, "weight"), (next_weight, "next_weight")):
+        if t is not None:
+            _given(t, name, (dim,), torch.float32, dev)
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    return rows, dim, dev, shape, _ACTIVATIONS[activation]
+
+
+def gdr_norm_gate(x, weight=None, gate=None, residual=None, next_weight=None, *, scale=1.0,
+                  eps=1e-6, activation="silu", y=None, y_norm=None, stream=None):
+    """y = residual + scale * act(gate) * norm(x) * weight and y_norm =
+    norm(y) * next_weight over the last dimension (see include/gdr.h).
+
+    x, gate, residual [..., dim] (bf16 or fp32); weight, next_weight [dim]
+    fp32; everything but x may be None; activation "silu", "sigmoid" or
+    "none".  ``y`` may be residual.  Returns (y, y_norm); y_norm is None
+    without next_weight.
+    """
+    rows, dim, dev, shape, act = _norm_args(x, weight, gate, residual, next_weight, activation)
+    if y is not None:
+        _given(y, "y", shape, x.dtype, dev)
+    if y_norm is not None:
+        if next_weight is None:
+            raise ValueError("y_norm needs next_weight")
+        _given(y_norm, "y_norm", shape, x.dtype, dev)
+    with _On(dev, stream) as on:
+        if y is None:
+            y = torch.empty(shape, dtype=x.dtype, device=dev)
+        if y_norm is None and next_weight is not None:
+            y_norm = torch.empty(shape, dtype=x.dtype, device=dev)
+        st = load_library().gdr_norm_gate(
+            _ptr(x), _ptr(weight), _ptr(gate), _ptr(residual), _ptr(next_weight), rows, dim,
+            float(scale), float(eps), act, _io_code(x.dtype), _ptr(y), _ptr(y_norm), on.ptr)
+    _check(st, "gdr_norm_gate")
+    return y, y_norm
+
+
+def gdr_norm_gate_workspace_size(rows, dim) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().gdr_norm_gate_workspace_size(rows, dim, ctypes.byref(n)),
+           "gdr_norm_gate_workspace_size")
+    return int(n.value)
+
+
+def gdr_norm_gate_backward(x, dy=None, dn=None, weight=None, gate=None, residual=None,
+                           next_weight=None, *, scale=1.0, eps=1e-6, activation="silu",
+                           workspace=None, stream=None):
+    """Gradient of <dy, y> + <dn, y_norm> of gdr_norm_gate (see include/gdr.h).
+
+    dy, dn like x, either None.  Returns (dx, dweight, dgate, dresidual,
+    dnext_weight): None for an input that was not given, and dnext_weight None
+    without dn.
+    """
+    rows, dim, dev, shape, act = _norm_args(x, weight, gate, residual, next_weight, activation)
+    if dy is None and dn is None:
+        raise ValueError("dy or dn is required")
+    for t, name in ((dy, "dy"), (dn, "dn")):
+        if t is not None:
+            _given(t, name, shape, x.dtype, dev)
+    if dn is not None and next_weight is None:
+        raise ValueError("dn needs next_weight")
+    with _On(dev, stream) as on:
+        new = lambda like: None if like is None else torch.empty_like(like)  # noqa: E731
+        dx, dweight, dgate, dres = new(x), new(weight), new(gate), new(residual)
+        dnext = new(next_weight) if dn is not None else None
+        need = 0 if dweight is None and dnext is None else gdr_norm_gate_workspace_size(rows, dim)
+        ws, ws_bytes, _keep = _scratch(workspace, need, dev)
+        st = load_library().gdr_norm_gate_backward(
+            _ptr(x), _ptr(weight), _ptr(gate), _ptr(residual), _ptr(next_weight), rows, dim,
+            float(scale), float(eps), act, _io_code(x.dtype), _ptr(dy), _ptr(dn), _ptr(dx),
+            _ptr(dweight), _ptr(dgate), _ptr(dres), _ptr(dnext), ws, ws_bytes, on.ptr)
+    _check(st, "gdr_norm_gate_backward")
+    return dx, dweight, dgate, dres, dnext

@@ -445,6 +445,129 @@ GDR_API gdr_status_t gdr_backward(const void *q, const void *k, const void *v, c
                                   float *d_initial_state, void *workspace,
                                   size_t workspace_bytes, void *stream);
 
+/*
+ * Linear attention with a decay for each head: the recurrence without the
+ * delta rule's correction, for layers whose heads forget at fixed rates,
+ *
+ *     S_t = e^{g_h} S_{t-1} + v_t k_t^T,    o_t = S_t q_t
+ *
+ * per (sequence, value head h), with the layouts, head grouping, packing and
+ * state [N, H, d_v, d_k] fp32 of the entry points above, so a model can mix
+ * both kinds of layers.  decay [H] fp32 holds the log-decays g_h <= 0, clamped
+ * at -20 like the gates above; they are constants of the layer (no gradient).
+ *
+ * gdr_linear_prefill runs whole prompts, gdr_linear_decode one token per
+ * sequence, gdr_linear_backward the gradient of
+ *
+ *     L = sum_t <d_o_t, o_t> + sum_n <d_final_state_n, final_state_n>
+ *
+ * with respect to q, k, v and the initial state.  d_o, dq, dk and dv are in
+ * the io dtype (each rounded once; dq and dk summed over the value heads of a
+ * group in fp32 before that), the states and their gradients fp32.  All sums
+ * run in a fixed order: the same inputs give the same bits.
+ *
+ * bf16 with d_k = d_v = 128 runs on the tensor cores: 64-token blocks, the
+ * score block and the copy of the state that meets the queries rounded to
+ * bf16, the state itself fp32 throughout.  Other shapes and fp32 run in fp32
+ * on the CUDA cores.  Infinities and NaN stay inside their (sequence, head);
+ * a non-finite value in v or k leaves NaN in every later output it reaches.
+ *
+ * cu_seqlens, initial_state, final_state (which may be initial_state) and
+ * empty sequences as for gdr_prefill_chunked; cu_seqlens needs 4-byte
+ * alignment.  workspace: 16-byte aligned, gdr_linear_workspace_size() bytes
+ * (`backward` nonzero for gdr_linear_backward); GDR_ERR_WORKSPACE below that.
+ * Calls that may overlap in time, captured ones among them, need workspaces
+ * of their own.  No output may overlap an input or another output.
+ */
+GDR_API gdr_status_t gdr_linear_workspace_size(int32_t num_seqs, int32_t total_T, int32_t H_qk,
+                                               int32_t H, int32_t d_k, int32_t d_v,
+                                               gdr_dtype_t io_dtype, int32_t backward,
+                                               size_t *bytes);
+
+GDR_API gdr_status_t gdr_linear_prefill(const void *q, const void *k, const void *v,
+                                        const float *decay, const float *initial_state,
+                                        const int32_t *cu_seqlens, int32_t num_seqs,
+                                        int32_t total_T, int32_t H_qk, int32_t H, int32_t d_k,
+                                        int32_t d_v, gdr_dtype_t io_dtype, void *o,
+                                        float *final_state, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+/* One token for each of N sequences: q, k [N, H_qk, d_k], v, o [N, H, d_v],
+ * state [N, H, d_v, d_k] read and overwritten in place. */
+GDR_API gdr_status_t gdr_linear_decode(const void *q, const void *k, const void *v,
+                                       const float *decay, float *state, int32_t N, int32_t H_qk,
+                                       int32_t H, int32_t d_k, int32_t d_v, gdr_dtype_t io_dtype,
+                                       void *o, void *stream);
+
+/* initial_state, d_final_state may be NULL (zeros), d_initial_state NULL (not wanted). */
+GDR_API gdr_status_t gdr_linear_backward(const void *q, const void *k, const void *v,
+                                         const float *decay, const float *initial_state,
+                                         const int32_t *cu_seqlens, int32_t num_seqs,
+                                         int32_t total_T, int32_t H_qk, int32_t H, int32_t d_k,
+                                         int32_t d_v, gdr_dtype_t io_dtype, const void *d_o,
+                                         const float *d_final_state, void *dq, void *dk, void *dv,
+                                         float *d_initial_state, void *workspace,
+                                         size_t workspace_bytes, void *stream);
+
+/*
+ * After a gdr_linear_prefill or gdr_linear_backward with this workspace:
+ * whether a bounded device-side wait in it gave up (GDR_ERR_DEVICE_TIMEOUT;
+ * its outputs are then not valid) or not (GDR_OK).  Synchronises `stream` and
+ * copies the call's status words.
+ */
+GDR_API gdr_status_t gdr_linear_check_workspace(const void *workspace, size_t workspace_bytes,
+                                                void *stream);
+
+/*
+ * Norms around a block, with its gate and residual scale, in one pass:
+ *
+ *     u = act(gate) * x / sqrt(mean(x^2) + eps) * weight
+ *     y = residual + scale * u
+ *     y_norm = y / sqrt(mean(y^2) + eps) * next_weight
+ *
+ * over rows of `dim` channels: [T, H, d_v] outputs of the recurrence with
+ * dim = d_v and rows = T * H give the gated output norm of a linear-attention
+ * layer; [T, hidden] with a residual gives the norm behind one block and the
+ * norm before the next.  weight NULL: x enters as it is.  gate NULL: no gate.
+ * residual NULL: y = scale * u.  next_weight and y_norm go together and may be
+ * NULL.  x, gate, residual, y, y_norm in the io dtype, weights fp32; the
+ * arithmetic is fp32 and y_norm is taken from y before its rounding.  y may be
+ * residual itself (updated in place); nothing else may overlap.
+ *
+ * dim is a multiple of 8, at most 16384; eps > 0; all pointers 16-byte aligned.
+ */
+typedef enum {
+    GDR_ACT_NONE = 0,      /* the gate multiplies as it is */
+    GDR_ACT_SILU = 1,
+    GDR_ACT_SIGMOID = 2
+} gdr_activation_t;
+
+GDR_API gdr_status_t gdr_norm_gate(const void *x, const float *weight, const void *gate,
+                                   const void *residual, const float *next_weight, int64_t rows,
+                                   int32_t dim, float scale, float eps,
+                                   gdr_activation_t activation, gdr_dtype_t io_dtype, void *y,
+                                   void *y_norm, void *stream);
+
+/*
+ * Gradient of sum <dy, y> + sum <dn, y_norm>.  dy or dn may be NULL (zero), not
+ * both.  dx, dgate, dresidual in the io dtype, dweight and dnext_weight fp32
+ * [dim], all overwritten.  dweight goes with weight, dgate with gate and
+ * dnext_weight with dn; dresidual may be NULL.  Inputs are those of the forward
+ * call; the rows' norms are recomputed.  workspace: 16-byte aligned,
+ * gdr_norm_gate_workspace_size() bytes, when a weight's gradient is wanted.  The
+ * sums over rows have a fixed order: the same inputs give the same bits.
+ */
+GDR_API gdr_status_t gdr_norm_gate_workspace_size(int64_t rows, int32_t dim, size_t *bytes);
+
+GDR_API gdr_status_t gdr_norm_gate_backward(const void *x, const float *weight, const void *gate,
+                                            const void *residual, const float *next_weight,
+                                            int64_t rows, int32_t dim, float scale, float eps,
+                                            gdr_activation_t activation, gdr_dtype_t io_dtype,
+                                            const void *dy, const void *dn, void *dx,
+                                            float *dweight, void *dgate, void *dresidual,
+                                            float *dnext_weight, void *workspace,
+                                            size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
