@@ -34,7 +34,10 @@ struct Costs {
     double block, state, cta, join;
 };
 
-Costs costs_of(int d_b, int d_v) {
+bool tensor_cores(int d_k, int d_v, bool bf16) { return bf16 && d_k == 128 && d_v == 128; }
+
+Costs costs_of(int d_b, int d_v, bool bf16) {
+    if (tensor_cores(d_b, d_v, bf16)) return Costs{kSMs, 1.6, 1.0, 5.0, 4.0};
     return Costs{kSMs * 2, 0.06 * d_b + 2.0, 0.04 * d_b + 2.0, 3.0, 4.0};
 }
 
@@ -42,8 +45,8 @@ Costs costs_of(int d_b, int d_v) {
 // one wave of segments after another.  Packed lengths are not known here:
 // about two segments for every place on the GPU bound what one long sequence
 // can cost, and shorter sequences stay whole.
-Plan make_plan(int N, int total_T, int H, int d_b, int d_v, bool equal) {
-    const Costs c = costs_of(d_b, d_v);
+Plan make_plan(int N, int total_T, int H, int d_b, int d_v, bool bf16, bool equal) {
+    const Costs c = costs_of(d_b, d_v, bf16);
     Plan p;
     if (!equal) {
         const int64_t blocks = ((int64_t)total_T + kScanBlock - 1) / kScanBlock;
@@ -94,12 +97,13 @@ Layout make_layout(const Plan &p, int N, int total_T, int H_qk, int H, int d_k, 
     return l;
 }
 
-size_t workspace_bytes(int N, int total_T, int H_qk, int H, int d_k, int d_v, bool backward) {
+size_t workspace_bytes(int N, int total_T, int H_qk, int H, int d_k, int d_v, bool bf16,
+                       bool backward) {
     if (N == 0 || total_T == 0) return 0;
     size_t most = 0;
     for (int equal = 0; equal < 2; ++equal) {
         if (equal && total_T % N != 0) continue;
-        const Plan p = make_plan(N, total_T, H, d_k, d_v, equal != 0);
+        const Plan p = make_plan(N, total_T, H, d_k, d_v, bf16, equal != 0);
         most = std::max(most, make_layout(p, N, total_T, H_qk, H, d_k, d_v, backward).total);
     }
     return most;
@@ -128,7 +132,7 @@ struct Call {
         p.seg = reinterpret_cast<float *>(ws + lay.seg);
         p.header = reinterpret_cast<uint32_t *>(ws);
         p.status = reinterpret_cast<uint32_t *>(ws + lay.status) + used;
-        p.status_words = 0;
+        p.status_words = tensor_cores(d_b, d_v, bf16) ? lay.words : 0;
         p.cu = cu;
         p.N = N; p.total_T = total_T; p.H = H;
         p.HA = HA; p.HB = HB; p.HV = HV;
@@ -148,6 +152,7 @@ struct Call {
     }
 
     cudaError_t pass(const ScanArgs &p, int d_b, int d_v, bool reverse, bool states, bool out_f32) {
+        if (tensor_cores(d_b, d_v, bf16)) return launch_scan_tc(p, reverse, states, out_f32, stream);
         return launch_scan_simt(p, d_b, d_v, reverse, states, bf16, out_f32, stream);
     }
 };
@@ -186,7 +191,8 @@ gdr_status_t gdr_linear_workspace_size(int32_t num_seqs, int32_t total_T, int32_
     if (bytes == nullptr) return GDR_ERR_INVALID_ARG;
     const gdr_status_t st = check_shape(num_seqs, total_T, H_qk, H, d_k, d_v, io_dtype, false);
     if (st != GDR_OK) return st;
-    *bytes = workspace_bytes(num_seqs, total_T, H_qk, H, d_k, d_v, backward != 0);
+    *bytes = workspace_bytes(num_seqs, total_T, H_qk, H, d_k, d_v, io_dtype == GDR_BF16,
+                             backward != 0);
     return GDR_OK;
 }
 
@@ -208,7 +214,7 @@ gdr_status_t gdr_linear_prefill(const void *q, const void *k, const void *v, con
     if (total_T > 0 && (!given16(q) || !given16(k) || !given16(v) || !given16(o) || decay == nullptr ||
                         !api::aligned(decay, 4)))
         return GDR_ERR_INVALID_ARG;
-    const Plan plan = total_T > 0 ? make_plan(num_seqs, total_T, H, d_k, d_v, equal) : Plan{kScanBlock, 0, 0};
+    const Plan plan = total_T > 0 ? make_plan(num_seqs, total_T, H, d_k, d_v, io_dtype == GDR_BF16, equal) : Plan{kScanBlock, 0, 0};
     const Layout lay = make_layout(plan, num_seqs, total_T, H_qk, H, d_k, d_v, false);
     const size_t need = total_T > 0 ? lay.total : 0;
     if (need > 0 && (!given16(workspace) || workspace_bytes < need)) return GDR_ERR_WORKSPACE;
@@ -292,7 +298,7 @@ gdr_status_t gdr_linear_backward(const void *q, const void *k, const void *v, co
     if (total_T > 0 && (!given16(q) || !given16(k) || !given16(v) || !given16(d_o) || !given16(dq) ||
                         !given16(dk) || !given16(dv) || decay == nullptr || !api::aligned(decay, 4)))
         return GDR_ERR_INVALID_ARG;
-    const Plan plan = total_T > 0 ? make_plan(num_seqs, total_T, H, d_k, d_v, equal) : Plan{kScanBlock, 0, 0};
+    const Plan plan = total_T > 0 ? make_plan(num_seqs, total_T, H, d_k, d_v, io_dtype == GDR_BF16, equal) : Plan{kScanBlock, 0, 0};
     const Layout lay = make_layout(plan, num_seqs, total_T, H_qk, H, d_k, d_v, true);
     const size_t need = total_T > 0 ? lay.total : 0;
     if (need > 0 && (!given16(workspace) || workspace_bytes < need)) return GDR_ERR_WORKSPACE;

@@ -135,6 +135,8 @@ __device__ inline Segment find_segment(const ScanArgs &p, int slot, bool inner, 
 
 // Launchers.  `states`: the pass that writes the segments' own states (all but
 // each sequence's last segment in scan order); otherwise the output pass.
+cudaError_t launch_scan_tc(const ScanArgs &p, bool reverse, bool states, bool out_f32,
+                           cudaStream_t stream);   // bf16, d_b = d_v = 128
 cudaError_t launch_scan_simt(const ScanArgs &p, int d_b, int d_v, bool reverse, bool states,
                              bool bf16, bool out_f32, cudaStream_t stream);
 // Segments' own states -> states behind each segment, in place.

@@ -1,0 +1,468 @@
+// Linear attention with a decay for each head on the tensor cores: bf16
+// inputs, d = 128, blocks of 64 tokens (the scan of linear_common.cuh).
+//
+// One CTA runs one segment of one (sequence, head) block after block.  With
+// x = e^g, i and j the rows of a block of n tokens and S the state entering it,
+//
+//     P   = (A B^T) .* M,            M_ij = x^|i-j| on the causal side, else 0
+//     O^T = (S A^T) diag(x^lead) + V^T P^T
+//     S  <- x^n S + (diag(w) V)^T B
+//     forward: lead = i + 1,     w_j = x^{n-1-j};   reverse: lead = n - 1 - i,  w_j = x^{j+1}
+//
+// Every exponent is >= 0 times g <= 0: nothing overflows however fast a head
+// decays.  All four products are tcgen05.mma with M = 128: O^T and S carry the
+// value channels on the TMEM lanes, so neither wastes half of the unit on 64
+// tokens, and S can be its own A operand from TMEM.
+//
+// Rounding.  A, B, V are exact bf16 operands.  P and the copy of S that meets A
+// are rounded to bf16: each adds about one output rounding to o, in
+// quadrature.  The state itself never is: it stays in fp32 registers, and
+// diag(w) V enters its product as three bf16 terms (24 significant bits), so
+// S is as exact as fp32 sums make it over any number of blocks.
+//
+// 16 warps: 0-1 turn the scores into P (one row a thread); 2 loads tiles by
+// TMA into a ring; 3 issues the MMAs; 4-7 split the weighted V and write O;
+// 8-15 hold S, 64 columns of one row a thread.  All but S -> S depends on the
+// block's tokens alone and runs ahead of it.
+#include "chunk_common.cuh"
+#include "linear_common.cuh"
+
+namespace gdr {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kSThreads = 256, kVThreads = 128, kPThreads = 64;
+
+constexpr uint32_t TILE = 16384;            // 64 tokens x 128 channels bf16, two 64-channel halves
+
+template <bool OUT>
+struct Shape {
+    static constexpr int NS = OUT ? 3 : 4;                   // tiles in the ring
+    static constexpr int NW = OUT ? 1 : 2;                   // buffers of the split V
+    static constexpr uint32_t STAGE = (OUT ? 3 : 2) * TILE;
+    static constexpr uint32_t B_OFF = OUT ? TILE : 0;        // A, B, V in a stage
+    static constexpr uint32_t V_OFF = B_OFF + TILE;
+    static constexpr uint32_t W_OFF = NS * STAGE;            // high, middle, low part
+    static constexpr uint32_t P_OFF = W_OFF + NW * 3 * TILE; // two buffers of 64 x 64 bf16
+    static constexpr uint32_t MISC = P_OFF + (OUT ? 2 * 8192 : 0);
+};
+
+struct Misc {
+    uint64_t full[4], stage_free[4];
+    uint64_t w_full[2], w_free[2];
+    uint64_t kv_full[2], kv_free[2];
+    uint64_t p_free[2];
+    uint64_t sc_full, p_full, s_full, s_free, o_full, o_free, end;
+    uint32_t tmem;
+    int abort;
+    int scratch[34];
+    float pw[kScanBlock + 1];
+};
+
+template <bool OUT>
+constexpr int smem_bytes() { return (int)(Shape<OUT>::MISC + sizeof(Misc)); }
+static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "shared memory");
+
+// TMEM columns
+constexpr uint32_t T_KV = 0;        // two buffers of 128
+constexpr uint32_t T_SC = 256;      // scores
+constexpr uint32_t T_OI = 320;      // S A^T
+constexpr uint32_t T_OA = 384;      // V^T P^T
+constexpr uint32_t T_SB = 448;      // S in bf16
+constexpr uint32_t T_COLS = 512;
+
+constexpr uint32_t ID_N64 = make_idesc(1, 128, 64);
+constexpr uint32_t ID_PV = ID_N64 | kIdescAMN;
+constexpr uint32_t ID_KV = make_idesc(1, 128, 128) | kIdescAMN | kIdescBMN;
+
+enum : uint32_t { E_ALIGN = 1, E_TMA = 2, E_MMA = 4, E_HANDOFF = 8 };
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&x);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+template <bool OUT, bool REV, typename OutT>
+__global__ void __launch_bounds__(kThreads, 1)
+scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+               const __grid_constant__ CUtensorMap mv, const ScanArgs p) {
+    using Sh = Shape<OUT>;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sbase = smem_u32(sm);
+    Misc *m = reinterpret_cast<Misc *>(sm + Sh::MISC);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int slot = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    uint32_t *status = p.status + blockIdx.x;
+    if (tid == 0) *status = 0;
+    if (OUT && blockIdx.x == 0 && tid == 0) *p.header = p.status_words;
+
+    const Segment seg = find_segment(p, slot, !OUT, REV, m->scratch, kThreads);
+    if (seg.n < 0) return;
+    const bool last = seg.index == seg.count - 1;
+    const int blocks = (seg.len + C - 1) / C;
+    const size_t state_at = ((size_t)seg.n * p.H + h) * (D * D);
+    float *seg_out = OUT ? nullptr : p.seg + ((size_t)seg.state * p.H + h) * (D * D);
+    // the state behind this segment: for the caller, for the join, or for nobody
+    const bool want_state = OUT ? (last && p.s_out != nullptr) : true;
+    if ((sbase & 1023u) != 0) {
+        if (tid == 0) atomicOr(status, E_ALIGN);
+        return;
+    }
+
+    if (tid == 0) {
+        for (int s = 0; s < 4; ++s) { mbar_init(&m->full[s], 1); mbar_init(&m->stage_free[s], 1); }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&m->w_full[b], kVThreads);
+            mbar_init(&m->w_free[b], 1);
+            mbar_init(&m->kv_full[b], 1);
+            mbar_init(&m->kv_free[b], kSThreads);
+            mbar_init(&m->p_free[b], 1);
+        }
+        mbar_init(&m->sc_full, 1);
+        mbar_init(&m->p_full, kPThreads);
+        mbar_init(&m->s_full, kSThreads);
+        mbar_init(&m->s_free, 1);
+        mbar_init(&m->o_full, 1);
+        mbar_init(&m->o_free, kVThreads);
+        mbar_init(&m->end, 1);
+        m->abort = 0;
+        fence_barrier_init();
+    }
+    const float g = clamp_log_gate(p.decay[h]);
+    if (tid <= C) m->pw[tid] = expf(g * (float)tid);
+    if (warp == 0) {
+        tmem_alloc(&m->tmem, T_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = m->tmem;
+    volatile int *abort = &m->abort;
+    auto fail = [&](uint32_t code) {
+        *abort = 1;
+        atomicOr(status, code);
+    };
+    // Bounded waits of one thread and of a whole warp (whose lanes then agree);
+    // false, and everyone told, when it gave up or another role did.
+    auto wait = [&](uint64_t *bar, uint32_t phase, uint32_t code) {
+        if (!mbar_wait_sleep(bar, phase & 1)) fail(code);
+        return *abort == 0;
+    };
+    auto warp_wait = [&](uint64_t *bar, uint32_t phase, uint32_t code) {
+        return __all_sync(0xffffffffu, wait(bar, phase, code)) != 0;
+    };
+    // block b in scan order: its first token and its tokens
+    auto block_t0 = [&](int b) { return seg.t0 + (REV ? blocks - 1 - b : b) * C; };
+    auto block_n = [&](int b) { return min(C, seg.len - (REV ? blocks - 1 - b : b) * C); };
+
+    if (warp >= 8) {
+        // ------------------------------------------------ S: row r, 64 columns ----
+        const int t = tid - kSThreads;
+        const int r = (warp & 3) * 32 + lane, half = (warp - 8) >> 2;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        float S[64];
+        if (OUT && seg.index > 0) {   // states between segments lie in the order of these threads
+            const float4 *src = reinterpret_cast<const float4 *>(
+                p.seg + ((size_t)(seg.state - 1) * p.H + h) * (D * D)) + t;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float4 x = src[i * kSThreads];
+                S[4 * i] = x.x; S[4 * i + 1] = x.y; S[4 * i + 2] = x.z; S[4 * i + 3] = x.w;
+            }
+        } else if (seg.index > 0 || p.s_in == nullptr) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) S[i] = 0.f;
+        } else if (p.turned) {
+            const float *src = p.s_in + state_at + (size_t)half * 64 * D + r;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) S[i] = src[i * D];
+        } else {
+            const float4 *src = reinterpret_cast<const float4 *>(p.s_in + state_at + r * D + half * 64);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float4 x = src[i];
+                S[4 * i] = x.x; S[4 * i + 1] = x.y; S[4 * i + 2] = x.z; S[4 * i + 3] = x.w;
+            }
+        }
+        bool ok = true;
+        for (int b = 0; b < blocks && ok; ++b) {
+            if (OUT) {
+                if (b > 0 && !(ok = warp_wait(&m->s_free, b - 1, E_MMA))) break;
+                tc_fence_after();
+                uint32_t x[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = pack_bf16(S[2 * i], S[2 * i + 1]);
+                tmem_st32(tmem + lanes + T_SB + half * 32, x);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&m->s_full);
+            }
+            if (b + 1 == blocks && !want_state) break;
+            if (!(ok = warp_wait(&m->kv_full[b & 1], b >> 1, E_MMA))) break;
+            tc_fence_after();
+            const float gn = REV || b + 1 == blocks ? m->pw[block_n(b)] : m->pw[C];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t x[16];
+                tmem_ld16(tmem + lanes + T_KV + (b & 1) * D + half * 64 + q * 16, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[q * 16 + i] = fmaf(gn, S[q * 16 + i], __uint_as_float(x[i]));
+            }
+            tc_fence_before();
+            mbar_arrive(&m->kv_free[b & 1]);
+        }
+        if (OUT) {
+            if (want_state) {
+                float4 *dst = reinterpret_cast<float4 *>(p.s_out + state_at + r * D + half * 64);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    dst[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+            }
+        } else {
+            float4 *dst = reinterpret_cast<float4 *>(seg_out) + t;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                dst[i * kSThreads] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+        }
+    } else if (warp >= 4) {
+        // ------------------------------- weighted V in three parts; O to memory ----
+        const int t = tid - 128;
+        const int r = t;                                    // value channel in the epilogue
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        bool ok = true;
+        auto write_out = [&](int b) {
+            if (!(ok = warp_wait(&m->o_full, b, E_MMA))) return;
+            tc_fence_after();
+            const int n = block_n(b);
+            OutT *dst = static_cast<OutT *>(p.out) + ((size_t)block_t0(b) * p.H + h) * D + r;
+            const size_t row = (size_t)p.H * D;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t xi[16], xa[16];
+                tmem_ld16(tmem + lanes + T_OI + q * 16, xi);
+                tmem_ld16(tmem + lanes + T_OA + q * 16, xa);
+                tmem_wait_ld();
+                if (q == 3) {
+                    tc_fence_before();
+                    mbar_arrive(&m->o_free);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int i = q * 16 + e;
+                    if (i < n) {
+                        const float lead = m->pw[REV ? n - 1 - i : i + 1];
+                        store_io(dst + i * row, fmaf(lead, __uint_as_float(xi[e]), __uint_as_float(xa[e])));
+                    }
+                }
+            }
+        };
+        for (int b = 0; b < blocks && ok; ++b) {
+            const int s = b % Sh::NS, w = b % Sh::NW, n = block_n(b);
+            if (!(ok = warp_wait(&m->full[s], b / Sh::NS, E_TMA))) break;
+            if (b >= Sh::NW && !(ok = warp_wait(&m->w_free[w], b / Sh::NW - 1, E_MMA))) break;
+            uint8_t *stage = sm + s * Sh::STAGE;
+            const bool need = b + 1 < blocks || want_state;
+            // rows behind the segment's last token hold another sequence's tokens (or
+            // anything): they leave B and V, since 0 * inf is not 0
+            if (n < C) {
+                for (int e = t; e < 2 * (C - n) * 8; e += kVThreads) {
+                    const uint32_t at = (e & 1) * 8192 + (n + (e >> 4)) * 128 + ((e >> 1) & 7) * 16;
+                    *reinterpret_cast<uint4 *>(stage + Sh::B_OFF + at) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(stage + Sh::V_OFF + at) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            if (need) {
+                uint8_t *wbuf = sm + Sh::W_OFF + w * 3 * TILE;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const uint32_t at = (uint32_t)(u * kVThreads + t) * 16;   // swizzled place: row in bits 7-12
+                    const int j = (at >> 7) & 63;
+                    const float wj = m->pw[REV ? j + 1 : max(n - 1 - j, 0)];
+                    uint4 x = *reinterpret_cast<const uint4 *>(stage + Sh::V_OFF + at);
+                    if (j >= n) x = make_uint4(0, 0, 0, 0);
+                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float f0 = bf16_lo(in[e]) * wj, f1 = bf16_hi(in[e]) * wj;
+                        hi[e] = pack_bf16(f0, f1);
+                        const float d0 = f0 - bf16_lo(hi[e]), d1 = f1 - bf16_hi(hi[e]);
+                        mid[e] = pack_bf16(d0, d1);
+                        lo[e] = pack_bf16(d0 - bf16_lo(mid[e]), d1 - bf16_hi(mid[e]));
+                    }
+                    *reinterpret_cast<uint4 *>(wbuf + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(wbuf + TILE + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                    *reinterpret_cast<uint4 *>(wbuf + 2 * TILE + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+            }
+            fence_proxy_async();
+            mbar_arrive(&m->w_full[w]);
+            if (OUT && b > 0) write_out(b - 1);
+        }
+        if (OUT && ok && blocks > 0) write_out(blocks - 1);
+    } else if (warp == 3) {
+        // ------------------------------------------------------- MMA issuer ----
+        if (lane == 0) {
+            bool ok = true;
+            auto scores = [&](int b) {
+                const int s = b % Sh::NS;
+                if (!(ok = wait(&m->full[s], b / Sh::NS, E_TMA))) return;
+                if (block_n(b) < C && !(ok = wait(&m->w_full[b % Sh::NW], b / Sh::NW, E_HANDOFF))) return;
+                tc_fence_after();
+                // rows 64 to 127 of A are what follows the tile: their scores are not read
+                const uint32_t st = sbase + s * Sh::STAGE;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_f16_ss(tmem + T_SC, sw128_kmajor_desc(st + (k >> 2) * 8192 + (k & 3) * 32),
+                               sw128_kmajor_desc(st + Sh::B_OFF + (k >> 2) * 8192 + (k & 3) * 32), ID_N64, k != 0);
+                mma_commit(&m->sc_full);
+            };
+            if (OUT && blocks > 0) scores(0);
+            for (int b = 0; b < blocks && ok; ++b) {
+                const int s = b % Sh::NS, w = b % Sh::NW;
+                const uint32_t st = sbase + s * Sh::STAGE;
+                if (!(ok = wait(&m->w_full[w], b / Sh::NW, E_HANDOFF))) break;
+                if (b + 1 < blocks || want_state) {
+                    if (b >= 2 && !(ok = wait(&m->kv_free[b & 1], (b >> 1) - 1, E_HANDOFF))) break;
+                    tc_fence_after();
+                    const uint32_t wb = sbase + Sh::W_OFF + w * 3 * TILE;
+#pragma unroll
+                    for (int part = 2; part >= 0; --part)     // the small terms first
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16_ss(tmem + T_KV + (b & 1) * D,
+                                       sw128_mnmajor_desc(wb + part * TILE + k * 2048, 8192, 1024),
+                                       sw128_mnmajor_desc(st + Sh::B_OFF + k * 2048, 8192, 1024), ID_KV,
+                                       part != 2 || k != 0);
+                    mma_commit(&m->kv_full[b & 1]);
+                }
+                mma_commit(&m->w_free[w]);
+                if (!OUT) {
+                    mma_commit(&m->stage_free[s]);
+                    continue;
+                }
+                if (!(ok = wait(&m->p_full, b, E_HANDOFF))) break;
+                if (b + 1 < blocks) {
+                    scores(b + 1);
+                    if (!ok) break;
+                }
+                if (!(ok = wait(&m->s_full, b, E_HANDOFF))) break;
+                if (b > 0 && !(ok = wait(&m->o_free, b - 1, E_HANDOFF))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_f16_ts(tmem + T_OI, tmem + T_SB + k * 8,
+                               sw128_kmajor_desc(st + (k >> 2) * 8192 + (k & 3) * 32), ID_N64, k != 0);
+                mma_commit(&m->s_free);
+                const uint32_t pb = sbase + Sh::P_OFF + (b & 1) * 8192;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_f16_ss(tmem + T_OA, sw128_mnmajor_desc(st + Sh::V_OFF + k * 2048, 8192, 1024),
+                               sw128_kmajor_desc(pb + k * 32), ID_PV, k != 0);
+                mma_commit(&m->o_full);
+                mma_commit(&m->p_free[b & 1]);
+                mma_commit(&m->stage_free[s]);
+            }
+            // every MMA issued here is complete before TMEM is freed
+            mma_commit(&m->end);
+            (void)mbar_wait_sleep(&m->end, 0);
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------ tile loader ----
+        if (lane == 0) {
+            const int ha = h / (p.H / p.HA), hb = h / (p.H / p.HB), hv = h / (p.H / p.HV);
+            int issued = 0;
+            for (int b = 0; b < blocks; ++b) {
+                const int s = b % Sh::NS;
+                if (b >= Sh::NS && !wait(&m->stage_free[s], b / Sh::NS - 1, E_MMA)) break;
+                if (*abort) break;
+                uint8_t *st = sm + s * Sh::STAGE;
+                const int t0 = block_t0(b);
+                mbar_arrive_expect_tx(&m->full[s], Sh::STAGE);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (OUT) tma_load_3d(st + x * 8192, &ma, &m->full[s], x * 64, ha, t0);
+                    tma_load_3d(st + Sh::B_OFF + x * 8192, &mb, &m->full[s], x * 64, hb, t0);
+                    tma_load_3d(st + Sh::V_OFF + x * 8192, &mv, &m->full[s], x * 64, hv, t0);
+                }
+                issued = b + 1;
+            }
+            // never leave a copy in flight into this CTA's shared memory
+            for (int b = issued > Sh::NS ? issued - Sh::NS : 0; b < issued; ++b)
+                (void)mbar_wait_sleep(&m->full[b % Sh::NS], (b / Sh::NS) & 1);
+        }
+    } else if (OUT) {
+        // ------------------------------------------- P = scores .* decay, row i ----
+        const int i = tid;
+        const uint32_t lanes = (uint32_t)warp << 21;
+        for (int b = 0; b < blocks; ++b) {
+            if (!warp_wait(&m->sc_full, b, E_MMA)) break;
+            if (b >= 2 && !warp_wait(&m->p_free[b & 1], (b >> 1) - 1, E_MMA)) break;
+            tc_fence_after();
+            const int n = block_n(b);
+            const uint32_t dst = sbase + Sh::P_OFF + (b & 1) * 8192;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t x[16], y[8];
+                tmem_ld16(tmem + lanes + T_SC + q * 16, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    float f[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int j = q * 16 + e + u, apart = REV ? j - i : i - j;
+                        f[u] = apart >= 0 && (!REV || j < n) ? __uint_as_float(x[e + u]) * m->pw[max(apart, 0)] : 0.f;
+                    }
+                    y[e >> 1] = pack_bf16(f[0], f[1]);
+                }
+                st_shared_v4(dst + sw128_offset(i, 2 * q), y[0], y[1], y[2], y[3]);
+                st_shared_v4(dst + sw128_offset(i, 2 * q + 1), y[4], y[5], y[6], y[7]);
+            }
+            tc_fence_before();
+            fence_proxy_async();
+            mbar_arrive(&m->p_full);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, T_COLS);
+    }
+}
+
+template <bool OUT, bool REV, typename OutT>
+cudaError_t launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mv,
+                   const ScanArgs &p, cudaStream_t stream) {
+    auto fn = scan_tc_kernel<OUT, REV, OutT>;
+    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(fn), smem_bytes<OUT>());
+    if (e != cudaSuccess) return e;
+    fn<<<(unsigned)(OUT ? p.slots : p.inner) * p.H, kThreads, smem_bytes<OUT>(), stream>>>(ma, mb, mv, p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_scan_tc(const ScanArgs &p, bool reverse, bool states, bool out_f32,
+                           cudaStream_t stream) {
+    CUtensorMap ma, mb, mv;
+    if (!make_map(&ma, p.a, p.total_T, p.HA) || !make_map(&mb, p.b, p.total_T, p.HB) ||
+        !make_map(&mv, p.v, p.total_T, p.HV))
+        return cudaErrorInvalidValue;
+    if (states)
+        return reverse ? launch<false, true, __nv_bfloat16>(ma, mb, mv, p, stream)
+                       : launch<false, false, __nv_bfloat16>(ma, mb, mv, p, stream);
+    if (out_f32)
+        return reverse ? launch<true, true, float>(ma, mb, mv, p, stream)
+                       : launch<true, false, float>(ma, mb, mv, p, stream);
+    return reverse ? launch<true, true, __nv_bfloat16>(ma, mb, mv, p, stream)
+                   : launch<true, false, __nv_bfloat16>(ma, mb, mv, p, stream);
+}
+
+}  // namespace gdr

@@ -109,7 +109,8 @@ def backward(q, k, v, decay, state, cu, N, d_o, d_final, bf16):
                                       ("v", (k[t, j], q[t, j], d_o[t, h], g, G, True), (t, h), dk)):
                 r, X, near, far, A = scan(*args)
                 out[name][0][at] += r
-                out[name][1][at] += bounds(r, near, far, L, d, bf16, rounded=group == 1)
+                # dv belongs to its value head alone and is rounded at once, dq and dk of a group after the sum
+                out[name][1][at] += bounds(r, near, far, L, d, bf16, rounded=group == 1 or name == "v")
                 if name == "v":
                     out["s"][0][n, h], out["s"][1][n, h] = X, fp32_terms(L, 0) * A
     if group > 1:   # the heads' sum, then the one rounding of dq and dk
