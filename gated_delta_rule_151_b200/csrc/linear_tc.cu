@@ -21,9 +21,11 @@
 // S is as exact as fp32 sums make it over any number of blocks.
 //
 // 16 warps: 0-1 turn the scores into P (one row a thread); 2 loads tiles by
-// TMA into a ring; 3 issues the MMAs; 4-7 split the weighted V and write O;
-// 8-15 hold S, 64 columns of one row a thread.  All but S -> S depends on the
+// TMA into a ring; 3 issues the MMAs; 4-7 write O; 8-15 hold S, 64 columns of
+// one row a thread, and split the weighted V.  All but S -> S depends on the
 // block's tokens alone and runs ahead of it.
+#include <cstddef>
+
 #include "chunk_common.cuh"
 #include "linear_common.cuh"
 
@@ -31,7 +33,7 @@ namespace gdr {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kSThreads = 256, kVThreads = 128, kPThreads = 64;
+constexpr int kSThreads = 256, kOThreads = 128, kPThreads = 64;
 
 constexpr uint32_t TILE = 16384;            // 64 tokens x 128 channels bf16, two 64-channel halves
 
@@ -44,30 +46,34 @@ struct Shape {
     static constexpr uint32_t V_OFF = B_OFF + TILE;
     static constexpr uint32_t W_OFF = NS * STAGE;            // high, middle, low part
     static constexpr uint32_t P_OFF = W_OFF + NW * 3 * TILE; // two buffers of 64 x 64 bf16
-    static constexpr uint32_t MISC = P_OFF + (OUT ? 2 * 8192 : 0);
+    static constexpr uint32_t O_OFF = P_OFF + (OUT ? 2 * 8192 : 0);   // a tile of O on its way out
+    static constexpr uint32_t MISC = O_OFF + (OUT ? TILE : 0);
 };
 
 struct Misc {
-    uint64_t full[4], stage_free[4];
-    uint64_t w_full[2], w_free[2];
-    uint64_t kv_full[2], kv_free[2];
-    uint64_t p_free[2];
-    uint64_t sc_full, p_full, s_full, s_free, o_full, o_free, end;
+    uint64_t full[4];                   // a stage's tiles have arrived
+    uint64_t w_full[2];                 // the split V is written
+    uint64_t kv_full[4], kv_free[2];    // its product is done (and its buffer free), and read
+    uint64_t sc_full[2], p_full[2];     // scores are done; P is written
+    uint64_t s_full;                    // S in bf16 is written
+    uint64_t done[3], o_free;           // every product of a block is done; O is read
+    uint64_t end;
     uint32_t tmem;
     int abort;
     int scratch[34];
-    float pw[kScanBlock + 1];
+    float pw[kScanBlock + 1];                // x^k
+    alignas(16) float lead[kScanBlock];                  // of S A^T in a full block
 };
 
+static_assert(Shape<true>::NS == 3 && Shape<false>::NS == 4, "copies of done and kv_full");
 template <bool OUT>
 constexpr int smem_bytes() { return (int)(Shape<OUT>::MISC + sizeof(Misc)); }
 static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "shared memory");
 
 // TMEM columns
 constexpr uint32_t T_KV = 0;        // two buffers of 128
-constexpr uint32_t T_SC = 256;      // scores
-constexpr uint32_t T_OI = 320;      // S A^T
-constexpr uint32_t T_OA = 384;      // V^T P^T
+constexpr uint32_t T_X = 256;       // two buffers of 64: a block's scores, then its V^T P^T
+constexpr uint32_t T_OI = 384;      // S A^T
 constexpr uint32_t T_SB = 448;      // S in bf16
 constexpr uint32_t T_COLS = 512;
 
@@ -76,6 +82,61 @@ constexpr uint32_t ID_PV = ID_N64 | kIdescAMN;
 constexpr uint32_t ID_KV = make_idesc(1, 128, 128) | kIdescAMN | kIdescBMN;
 
 enum : uint32_t { E_ALIGN = 1, E_TMA = 2, E_MMA = 4, E_HANDOFF = 8 };
+
+// Parity cannot tell a barrier's phase from the one two later, so a barrier whose
+// owner can run ahead of a waiter has several copies, one block after another:
+// enough that a copy's next phase needs that waiter to have gone on.  Commits are
+// few (each holds the issuer up by 200 cycles): one barrier can have many waiters.
+
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t phase) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(phase)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The rest of a wait whose first look found its phase unfinished: polls, a
+// bounded number of times, until the phase completes or some role has given up
+// (at `abort`).  Called by whole warps; kept out of line, as every wait has one.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t phase, uint32_t abort) {
+    for (uint32_t it = 0; it < (1u << 21); ++it) {
+        const bool ok = try_wait(bar, phase);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        uint32_t stop;
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(stop) : "r"(abort) : "memory");
+        if (__any_sync(0xffffffffu, stop != 0)) return false;
+    }
+    return false;
+}
+
+// Whether any thread of a group of whole warps says stop; all of them come here.
+__device__ __forceinline__ bool group_stop(int id, int threads, bool stop) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred pc, pr;\n\t"
+        "setp.ne.u32 pc, %1, 0;\n\t"
+        "barrier.red.or.pred pr, %2, %3, pc;\n\t"
+        "selp.u32 %0, 1, 0, pr;\n\t}"
+        : "=r"(any)
+        : "r"((uint32_t)stop), "r"(id), "r"(threads)
+        : "memory");
+    return any != 0;
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
@@ -111,27 +172,32 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         return;
     }
 
+    if (tid == 64) {
+        if (OUT) prefetch_tensormap(&ma);
+        prefetch_tensormap(&mb);
+        prefetch_tensormap(&mv);
+    }
     if (tid == 0) {
-        for (int s = 0; s < 4; ++s) { mbar_init(&m->full[s], 1); mbar_init(&m->stage_free[s], 1); }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&m->w_full[b], kVThreads);
-            mbar_init(&m->w_free[b], 1);
-            mbar_init(&m->kv_full[b], 1);
-            mbar_init(&m->kv_free[b], kSThreads);
-            mbar_init(&m->p_free[b], 1);
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(&m->full[s], 1);
+            mbar_init(&m->kv_full[s], 1);
         }
-        mbar_init(&m->sc_full, 1);
-        mbar_init(&m->p_full, kPThreads);
+        for (int s = 0; s < 3; ++s) mbar_init(&m->done[s], 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&m->w_full[b], kSThreads);
+            mbar_init(&m->kv_free[b], kSThreads);
+            mbar_init(&m->sc_full[b], 1);
+            mbar_init(&m->p_full[b], kPThreads);
+        }
         mbar_init(&m->s_full, kSThreads);
-        mbar_init(&m->s_free, 1);
-        mbar_init(&m->o_full, 1);
-        mbar_init(&m->o_free, kVThreads);
+        mbar_init(&m->o_free, kOThreads);
         mbar_init(&m->end, 1);
         m->abort = 0;
         fence_barrier_init();
     }
     const float g = clamp_log_gate(p.decay[h]);
     if (tid <= C) m->pw[tid] = expf(g * (float)tid);
+    if (tid < C) m->lead[tid] = expf(g * (float)(REV ? C - 1 - tid : tid + 1));
     if (warp == 0) {
         tmem_alloc(&m->tmem, T_COLS);
         tmem_relinquish();
@@ -140,19 +206,18 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m->tmem;
-    volatile int *abort = &m->abort;
-    auto fail = [&](uint32_t code) {
-        *abort = 1;
-        atomicOr(status, code);
-    };
-    // Bounded waits of one thread and of a whole warp (whose lanes then agree);
-    // false, and everyone told, when it gave up or another role did.
-    auto wait = [&](uint64_t *bar, uint32_t phase, uint32_t code) {
-        if (!mbar_wait_sleep(bar, phase & 1)) fail(code);
-        return *abort == 0;
-    };
-    auto warp_wait = [&](uint64_t *bar, uint32_t phase, uint32_t code) {
-        return __all_sync(0xffffffffu, wait(bar, phase, code)) != 0;
+    const uint32_t mbase = sbase + Sh::MISC;
+#define BAR(name, i) (mbase + (uint32_t)offsetof(Misc, name) + 8 * (i))
+    // Bounded wait of a whole warp; false, and everyone told, when it or another role
+    // gave up.  A phase that is complete already costs one look.
+    auto warp_wait = [&](uint32_t bar, uint32_t phase, uint32_t code) {
+        if (__all_sync(0xffffffffu, try_wait(bar, phase & 1))) return true;
+        if (wait_on(bar, phase & 1, BAR(abort, 0))) return true;
+        if (lane == 0) {
+            *reinterpret_cast<volatile int *>(&m->abort) = 1;
+            atomicOr(status, code);
+        }
+        return false;
     };
     // block b in scan order: its first token and its tokens
     auto block_t0 = [&](int b) { return seg.t0 + (REV ? blocks - 1 - b : b) * C; };
@@ -188,9 +253,54 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             }
         }
         bool ok = true;
+        // diag(w) V of block b in three bf16 parts, in the tile's own layout
+        auto split_v = [&](int b) {
+            const int s = b % Sh::NS, w = b % Sh::NW, n = block_n(b);
+            if (!(ok = warp_wait(BAR(full, s), b / Sh::NS, E_TMA))) return;
+            if (b >= Sh::NW && !(ok = warp_wait(BAR(kv_full, (b - Sh::NW) & 3), (b - Sh::NW) >> 2, E_MMA))) return;
+            uint8_t *stage = sm + s * Sh::STAGE;
+            // rows behind the segment's last token hold another sequence's tokens (or
+            // anything): they leave B and V, since 0 * inf is not 0
+            if (n < C) {
+                for (int e = t; e < 2 * (C - n) * 8; e += kSThreads) {
+                    const uint32_t at = (e & 1) * 8192 + (n + (e >> 4)) * 128 + ((e >> 1) & 7) * 16;
+                    *reinterpret_cast<uint4 *>(stage + Sh::B_OFF + at) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(stage + Sh::V_OFF + at) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            if (b + 1 < blocks || want_state) {
+                uint8_t *wbuf = sm + Sh::W_OFF + w * 3 * TILE;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t at = (uint32_t)(u * kSThreads + t) * 16;   // swizzled place: row in bits 7-12
+                    const int j = (at >> 7) & 63;
+                    const float wj = m->pw[REV ? j + 1 : max(n - 1 - j, 0)];
+                    const float2 w2 = make_float2(wj, wj), minus = make_float2(-1.f, -1.f);
+                    uint4 x = *reinterpret_cast<const uint4 *>(stage + Sh::V_OFF + at);
+                    if (j >= n) x = make_uint4(0, 0, 0, 0);
+                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float2 f = __fmul2_rn(make_float2(bf16_lo(in[e]), bf16_hi(in[e])), w2);
+                        hi[e] = pack_bf16(f.x, f.y);
+                        f = __ffma2_rn(make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])), minus, f);
+                        mid[e] = pack_bf16(f.x, f.y);
+                        f = __ffma2_rn(make_float2(bf16_lo(mid[e]), bf16_hi(mid[e])), minus, f);
+                        lo[e] = pack_bf16(f.x, f.y);
+                    }
+                    *reinterpret_cast<uint4 *>(wbuf + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(wbuf + TILE + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                    *reinterpret_cast<uint4 *>(wbuf + 2 * TILE + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+            }
+            fence_proxy_async();
+            arrive(BAR(w_full, w));
+        };
+        if (blocks > 0) split_v(0);
         for (int b = 0; b < blocks && ok; ++b) {
             if (OUT) {
-                if (b > 0 && !(ok = warp_wait(&m->s_free, b - 1, E_MMA))) break;
+                if (b > 0 && !(ok = warp_wait(BAR(done, (b - 1) % 3), (b - 1) / 3, E_MMA))) break;
                 tc_fence_after();
                 uint32_t x[32];
 #pragma unroll
@@ -198,10 +308,14 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                 tmem_st32(tmem + lanes + T_SB + half * 32, x);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&m->s_full);
+                arrive(BAR(s_full, 0));
+            }
+            if (b + 1 < blocks) {
+                split_v(b + 1);
+                if (!ok) break;
             }
             if (b + 1 == blocks && !want_state) break;
-            if (!(ok = warp_wait(&m->kv_full[b & 1], b >> 1, E_MMA))) break;
+            if (!(ok = warp_wait(BAR(kv_full, b & 3), b >> 2, E_MMA))) break;
             tc_fence_after();
             const float gn = REV || b + 1 == blocks ? m->pw[block_n(b)] : m->pw[C];
 #pragma unroll
@@ -213,7 +327,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                 for (int i = 0; i < 16; ++i) S[q * 16 + i] = fmaf(gn, S[q * 16 + i], __uint_as_float(x[i]));
             }
             tc_fence_before();
-            mbar_arrive(&m->kv_free[b & 1]);
+            arrive(BAR(kv_free, b & 1));
         }
         if (OUT) {
             if (want_state) {
@@ -229,157 +343,139 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                 dst[i * kSThreads] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
         }
     } else if (warp >= 4) {
-        // ------------------------------- weighted V in three parts; O to memory ----
-        const int t = tid - 128;
-        const int r = t;                                    // value channel in the epilogue
+        // --------------------------------------- O: value channel r, all tokens ----
+        const int r = tid - 128;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-        bool ok = true;
-        auto write_out = [&](int b) {
-            if (!(ok = warp_wait(&m->o_full, b, E_MMA))) return;
+        const size_t row = (size_t)p.H * D;
+        OutT *tile = reinterpret_cast<OutT *>(sm + Sh::O_OFF) + r;
+        for (int b = 0; OUT && b < blocks; ++b) {
+            constexpr bool kTile = sizeof(OutT) == 2;
+            const bool ok = warp_wait(BAR(done, b % 3), b / 3, E_MMA);
+            // bf16 goes through a tile and leaves 16 bytes a thread: 2-byte stores from
+            // the lanes' channels took 3,400 cycles a block, one bulk copy a row 2,600
+            if (group_stop(1, kOThreads, !ok)) break;   // (and the last tile has left)
             tc_fence_after();
             const int n = block_n(b);
-            OutT *dst = static_cast<OutT *>(p.out) + ((size_t)block_t0(b) * p.H + h) * D + r;
-            const size_t row = (size_t)p.H * D;
+            OutT *dst = static_cast<OutT *>(p.out) + ((size_t)block_t0(b) * p.H + h) * D;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint32_t xi[16], xa[16];
+                float lead[16];
                 tmem_ld16(tmem + lanes + T_OI + q * 16, xi);
-                tmem_ld16(tmem + lanes + T_OA + q * 16, xa);
+                tmem_ld16(tmem + lanes + T_X + (b & 1) * 64 + q * 16, xa);
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    *reinterpret_cast<float4 *>(lead + e) = *reinterpret_cast<const float4 *>(m->lead + q * 16 + e);
+                if (REV && n < C) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) lead[e] = m->pw[max(n - 1 - (q * 16 + e), 0)];
+                }
                 tmem_wait_ld();
                 if (q == 3) {
                     tc_fence_before();
-                    mbar_arrive(&m->o_free);
+                    arrive(BAR(o_free, 0));
                 }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int i = q * 16 + e;
-                    if (i < n) {
-                        const float lead = m->pw[REV ? n - 1 - i : i + 1];
-                        store_io(dst + i * row, fmaf(lead, __uint_as_float(xi[e]), __uint_as_float(xa[e])));
-                    }
+                    const float o = fmaf(lead[e], __uint_as_float(xi[e]), __uint_as_float(xa[e]));
+                    if (kTile) store_io(tile + i * D, o);
+                    else if (i < n) store_io(dst + i * row + r, o);
                 }
             }
-        };
-        for (int b = 0; b < blocks && ok; ++b) {
-            const int s = b % Sh::NS, w = b % Sh::NW, n = block_n(b);
-            if (!(ok = warp_wait(&m->full[s], b / Sh::NS, E_TMA))) break;
-            if (b >= Sh::NW && !(ok = warp_wait(&m->w_free[w], b / Sh::NW - 1, E_MMA))) break;
-            uint8_t *stage = sm + s * Sh::STAGE;
-            const bool need = b + 1 < blocks || want_state;
-            // rows behind the segment's last token hold another sequence's tokens (or
-            // anything): they leave B and V, since 0 * inf is not 0
-            if (n < C) {
-                for (int e = t; e < 2 * (C - n) * 8; e += kVThreads) {
-                    const uint32_t at = (e & 1) * 8192 + (n + (e >> 4)) * 128 + ((e >> 1) & 7) * 16;
-                    *reinterpret_cast<uint4 *>(stage + Sh::B_OFF + at) = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4 *>(stage + Sh::V_OFF + at) = make_uint4(0, 0, 0, 0);
-                }
-            }
-            if (need) {
-                uint8_t *wbuf = sm + Sh::W_OFF + w * 3 * TILE;
+            if (kTile) {
+                if (group_stop(1, kOThreads, false)) break;
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    const uint32_t at = (uint32_t)(u * kVThreads + t) * 16;   // swizzled place: row in bits 7-12
-                    const int j = (at >> 7) & 63;
-                    const float wj = m->pw[REV ? j + 1 : max(n - 1 - j, 0)];
-                    uint4 x = *reinterpret_cast<const uint4 *>(stage + Sh::V_OFF + at);
-                    if (j >= n) x = make_uint4(0, 0, 0, 0);
-                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t hi[4], mid[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float f0 = bf16_lo(in[e]) * wj, f1 = bf16_hi(in[e]) * wj;
-                        hi[e] = pack_bf16(f0, f1);
-                        const float d0 = f0 - bf16_lo(hi[e]), d1 = f1 - bf16_hi(hi[e]);
-                        mid[e] = pack_bf16(d0, d1);
-                        lo[e] = pack_bf16(d0 - bf16_lo(mid[e]), d1 - bf16_hi(mid[e]));
-                    }
-                    *reinterpret_cast<uint4 *>(wbuf + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(wbuf + TILE + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                    *reinterpret_cast<uint4 *>(wbuf + 2 * TILE + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    const int e = u * kOThreads + r, i = e >> 4;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(sm + Sh::O_OFF + e * 16);
+                    if (i < n) *reinterpret_cast<uint4 *>(dst + i * row + (e & 15) * 8) = x;
                 }
             }
-            fence_proxy_async();
-            mbar_arrive(&m->w_full[w]);
-            if (OUT && b > 0) write_out(b - 1);
         }
-        if (OUT && ok && blocks > 0) write_out(blocks - 1);
     } else if (warp == 3) {
         // ------------------------------------------------------- MMA issuer ----
-        if (lane == 0) {
-            bool ok = true;
-            auto scores = [&](int b) {
-                const int s = b % Sh::NS;
-                if (!(ok = wait(&m->full[s], b / Sh::NS, E_TMA))) return;
-                if (block_n(b) < C && !(ok = wait(&m->w_full[b % Sh::NW], b / Sh::NW, E_HANDOFF))) return;
-                tc_fence_after();
-                // rows 64 to 127 of A are what follows the tile: their scores are not read
-                const uint32_t st = sbase + s * Sh::STAGE;
+        // The warp stays together and one elected lane issues, so that descriptors
+        // are uniform values: an operand's base, plus a constant for each step.
+        bool ok = true;
+        const uint64_t ka = sw128_kmajor_desc(sbase), mn = sw128_mnmajor_desc(sbase, 8192, 1024);
+        auto scores = [&](int b) {
+            const int s = b % Sh::NS;
+            if (!(ok = warp_wait(BAR(full, s), b / Sh::NS, E_TMA))) return;
+            if (block_n(b) < C && !(ok = warp_wait(BAR(w_full, b % Sh::NW), b / Sh::NW, E_HANDOFF))) return;
+            // the buffer last held block b - 2's V^T P^T
+            if (b >= 2 && !(ok = warp_wait(BAR(o_free, 0), b - 2, E_HANDOFF))) return;
+            tc_fence_after();
+            // rows 64 to 127 of A are what follows the tile: their scores are not read
+            const uint64_t at = ka + ((s * Sh::STAGE) >> 4);
+            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_f16_ss(tmem + T_SC, sw128_kmajor_desc(st + (k >> 2) * 8192 + (k & 3) * 32),
-                               sw128_kmajor_desc(st + Sh::B_OFF + (k >> 2) * 8192 + (k & 3) * 32), ID_N64, k != 0);
-                mma_commit(&m->sc_full);
-            };
-            if (OUT && blocks > 0) scores(0);
-            for (int b = 0; b < blocks && ok; ++b) {
-                const int s = b % Sh::NS, w = b % Sh::NW;
-                const uint32_t st = sbase + s * Sh::STAGE;
-                if (!(ok = wait(&m->w_full[w], b / Sh::NW, E_HANDOFF))) break;
-                if (b + 1 < blocks || want_state) {
-                    if (b >= 2 && !(ok = wait(&m->kv_free[b & 1], (b >> 1) - 1, E_HANDOFF))) break;
-                    tc_fence_after();
-                    const uint32_t wb = sbase + Sh::W_OFF + w * 3 * TILE;
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t step = ((k >> 2) * 8192 + (k & 3) * 32) >> 4;
+                    mma_f16_ss(tmem + T_X + (b & 1) * 64, at + step, at + (Sh::B_OFF >> 4) + step, ID_N64, k != 0);
+                }
+                mma_commit(&m->sc_full[b & 1]);
+            }
+            __syncwarp();
+        };
+        if (OUT && blocks > 0) scores(0);
+        for (int b = 0; b < blocks && ok; ++b) {
+            const int s = b % Sh::NS, w = b % Sh::NW;
+            const uint32_t st = (s * Sh::STAGE) >> 4;
+            const bool kv = b + 1 < blocks || want_state;
+            if (!(ok = warp_wait(BAR(w_full, w), b / Sh::NW, E_HANDOFF))) break;
+            if (kv && b >= 2 && !(ok = warp_wait(BAR(kv_free, b & 1), (b >> 1) - 1, E_HANDOFF))) break;
+            tc_fence_after();
+            if (elect_one()) {
+                if (kv) {
+                    const uint64_t wd = mn + ((Sh::W_OFF + w * 3 * TILE) >> 4), bd = mn + (st + (Sh::B_OFF >> 4));
+                    const uint32_t d = tmem + T_KV + (b & 1) * D;
 #pragma unroll
                     for (int part = 2; part >= 0; --part)     // the small terms first
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_f16_ss(tmem + T_KV + (b & 1) * D,
-                                       sw128_mnmajor_desc(wb + part * TILE + k * 2048, 8192, 1024),
-                                       sw128_mnmajor_desc(st + Sh::B_OFF + k * 2048, 8192, 1024), ID_KV,
+                            mma_f16_ss(d, wd + ((part * TILE + k * 2048) >> 4), bd + ((k * 2048) >> 4), ID_KV,
                                        part != 2 || k != 0);
-                    mma_commit(&m->kv_full[b & 1]);
+                    mma_commit(&m->kv_full[b & 3]);
                 }
-                mma_commit(&m->w_free[w]);
-                if (!OUT) {
-                    mma_commit(&m->stage_free[s]);
-                    continue;
-                }
-                if (!(ok = wait(&m->p_full, b, E_HANDOFF))) break;
-                if (b + 1 < blocks) {
-                    scores(b + 1);
-                    if (!ok) break;
-                }
-                if (!(ok = wait(&m->s_full, b, E_HANDOFF))) break;
-                if (b > 0 && !(ok = wait(&m->o_free, b - 1, E_HANDOFF))) break;
-                tc_fence_after();
+            }
+            __syncwarp();
+            if (!OUT) continue;
+            if (b + 1 < blocks) {
+                scores(b + 1);
+                if (!ok) break;
+            }
+            if (!(ok = warp_wait(BAR(s_full, 0), b, E_HANDOFF))) break;
+            if (!(ok = warp_wait(BAR(p_full, b & 1), b >> 1, E_HANDOFF))) break;
+            if (b + 1 == blocks && b > 0 && !(ok = warp_wait(BAR(o_free, 0), b - 1, E_HANDOFF))) break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t ad = ka + st, vd = mn + (st + (Sh::V_OFF >> 4));
+                const uint64_t pd = ka + ((Sh::P_OFF + (b & 1) * 8192) >> 4);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    mma_f16_ts(tmem + T_OI, tmem + T_SB + k * 8,
-                               sw128_kmajor_desc(st + (k >> 2) * 8192 + (k & 3) * 32), ID_N64, k != 0);
-                mma_commit(&m->s_free);
-                const uint32_t pb = sbase + Sh::P_OFF + (b & 1) * 8192;
+                    mma_f16_ts(tmem + T_OI, tmem + T_SB + k * 8, ad + (((k >> 2) * 8192 + (k & 3) * 32) >> 4),
+                               ID_N64, k != 0);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_f16_ss(tmem + T_OA, sw128_mnmajor_desc(st + Sh::V_OFF + k * 2048, 8192, 1024),
-                               sw128_kmajor_desc(pb + k * 32), ID_PV, k != 0);
-                mma_commit(&m->o_full);
-                mma_commit(&m->p_free[b & 1]);
-                mma_commit(&m->stage_free[s]);
+                    mma_f16_ss(tmem + T_X + (b & 1) * 64, vd + ((k * 2048) >> 4), pd + ((k * 32) >> 4), ID_PV, k != 0);
+                mma_commit(&m->done[s]);
             }
-            // every MMA issued here is complete before TMEM is freed
-            mma_commit(&m->end);
-            (void)mbar_wait_sleep(&m->end, 0);
+            __syncwarp();
         }
+        // every MMA issued here is complete before TMEM is freed
+        if (elect_one()) mma_commit(&m->end);
+        __syncwarp();
+        (void)mbar_wait_sleep(&m->end, 0);
     } else if (warp == 2) {
         // ------------------------------------------------------ tile loader ----
-        if (lane == 0) {
-            const int ha = h / (p.H / p.HA), hb = h / (p.H / p.HB), hv = h / (p.H / p.HV);
-            int issued = 0;
-            for (int b = 0; b < blocks; ++b) {
-                const int s = b % Sh::NS;
-                if (b >= Sh::NS && !wait(&m->stage_free[s], b / Sh::NS - 1, E_MMA)) break;
-                if (*abort) break;
+        const int ha = h / (p.H / p.HA), hb = h / (p.H / p.HB), hv = h / (p.H / p.HV);
+        int issued = 0;
+        for (int b = 0; b < blocks; ++b) {
+            const int s = b % Sh::NS;
+            // a stage is free when the products that read it are done
+            if (b >= Sh::NS && !warp_wait(OUT ? BAR(done, s) : BAR(kv_full, s), b / Sh::NS - 1, E_MMA)) break;
+            if (elect_one()) {
                 uint8_t *st = sm + s * Sh::STAGE;
                 const int t0 = block_t0(b);
                 mbar_arrive_expect_tx(&m->full[s], Sh::STAGE);
@@ -389,43 +485,60 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                     tma_load_3d(st + Sh::B_OFF + x * 8192, &mb, &m->full[s], x * 64, hb, t0);
                     tma_load_3d(st + Sh::V_OFF + x * 8192, &mv, &m->full[s], x * 64, hv, t0);
                 }
-                issued = b + 1;
             }
-            // never leave a copy in flight into this CTA's shared memory
-            for (int b = issued > Sh::NS ? issued - Sh::NS : 0; b < issued; ++b)
-                (void)mbar_wait_sleep(&m->full[b % Sh::NS], (b / Sh::NS) & 1);
+            __syncwarp();
+            issued = b + 1;
         }
+        // never leave a copy in flight into this CTA's shared memory
+        for (int b = issued > Sh::NS ? issued - Sh::NS : 0; b < issued; ++b)
+            (void)mbar_wait_sleep(&m->full[b % Sh::NS], (b / Sh::NS) & 1);
     } else if (OUT) {
         // ------------------------------------------- P = scores .* decay, row i ----
         const int i = tid;
         const uint32_t lanes = (uint32_t)warp << 21;
+        // with i = 8 I + f, j = 8 J + e: x^|i-j| = x^{8|I-J|} x^{|f-e|} where e lies on f's
+        // causal side, else x^{8(|I-J|-1)} x^{8-|f-e|}: sixteen factors a thread, two a group
+        const int I = i >> 3, f = i & 7;
+        float near[8], far[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int apart = REV ? e - f : f - e;
+            near[e] = apart >= 0 ? m->pw[apart] : 0.f;
+            far[e] = apart < 0 ? m->pw[8 + apart] : 0.f;
+        }
         for (int b = 0; b < blocks; ++b) {
-            if (!warp_wait(&m->sc_full, b, E_MMA)) break;
-            if (b >= 2 && !warp_wait(&m->p_free[b & 1], (b >> 1) - 1, E_MMA)) break;
+            if (!warp_wait(BAR(sc_full, b & 1), b >> 1, E_MMA)) break;
+            if (b >= 2 && !warp_wait(BAR(done, (b - 2) % 3), (b - 2) / 3, E_MMA)) break;
             tc_fence_after();
             const int n = block_n(b);
             const uint32_t dst = sbase + Sh::P_OFF + (b & 1) * 8192;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t x[16], y[8];
-                tmem_ld16(tmem + lanes + T_SC + q * 16, x);
+            for (int half = 0; half < 2; ++half) {
+                uint32_t x[32];
+                tmem_ld32(tmem + lanes + T_X + (b & 1) * 64 + half * 32, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    float f[2];
+                for (int q = 0; q < 4; ++q) {
+                    const int J = half * 4 + q, G = REV ? J - I : I - J;
+                    const float g0 = G >= 0 ? m->pw[8 * max(G, 0)] : 0.f;
+                    const float g1 = G >= 1 ? m->pw[8 * max(G - 1, 0)] : 0.f;
+                    const float2 m0 = make_float2(g0, g0), m1 = make_float2(g1, g1);
+                    uint32_t y[4];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int j = q * 16 + e + u, apart = REV ? j - i : i - j;
-                        f[u] = apart >= 0 && (!REV || j < n) ? __uint_as_float(x[e + u]) * m->pw[max(apart, 0)] : 0.f;
+                    for (int e = 0; e < 8; e += 2) {
+                        const float2 w = __ffma2_rn(make_float2(far[e], far[e + 1]), m1,
+                                                    __fmul2_rn(make_float2(near[e], near[e + 1]), m0));
+                        const float2 s = __fmul2_rn(make_float2(__uint_as_float(x[q * 8 + e]), __uint_as_float(x[q * 8 + e + 1])), w);
+                        const int j = J * 8 + e;     // masked by selection: a score may be anything there
+                        y[e >> 1] = pack_bf16((REV ? j >= i && j < n : j <= i) ? s.x : 0.f,
+                                              (REV ? j + 1 >= i && j + 1 < n : j + 1 <= i) ? s.y : 0.f);
                     }
-                    y[e >> 1] = pack_bf16(f[0], f[1]);
+                    st_shared_v4(dst + sw128_offset(i, J), y[0], y[1], y[2], y[3]);
                 }
-                st_shared_v4(dst + sw128_offset(i, 2 * q), y[0], y[1], y[2], y[3]);
-                st_shared_v4(dst + sw128_offset(i, 2 * q + 1), y[4], y[5], y[6], y[7]);
             }
             tc_fence_before();
             fence_proxy_async();
-            mbar_arrive(&m->p_full);
+            arrive(BAR(p_full, b & 1));
         }
     }
 
