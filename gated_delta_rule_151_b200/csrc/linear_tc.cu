@@ -20,10 +20,11 @@
 // diag(w) V enters its product as three bf16 terms (24 significant bits), so
 // S is as exact as fp32 sums make it over any number of blocks.
 //
-// 16 warps: 0-1 turn the scores into P (one row a thread); 2 loads tiles by
-// TMA into a ring; 3 issues the MMAs; 4-7 write O; 8-15 hold S, 64 columns of
-// one row a thread, and split the weighted V.  All but S -> S depends on the
-// block's tokens alone and runs ahead of it.
+// 16 warps: 0-1 turn the scores into P (one row a thread); 2 issues the products
+// of a block's tokens alone (scores, (diag(w) V)^T B), 3 starts the TMA loads into
+// a ring of tiles (each takes its issuer 300 cycles) and issues the products that
+// wait for S and P; 4-7 write O; 8-15 hold S, 64 columns of one row a thread, and
+// split the weighted V.  The pass that only wants the state uses 2, 3 and 8-15.
 #include <cstddef>
 
 #include "chunk_common.cuh"
@@ -56,8 +57,8 @@ struct Misc {
     uint64_t kv_full[4], kv_free[2];    // its product is done (and its buffer free), and read
     uint64_t sc_full[2], p_full[2];     // scores are done; P is written
     uint64_t s_full;                    // S in bf16 is written
-    uint64_t done[3], o_free;           // every product of a block is done; O is read
-    uint64_t end;
+    uint64_t done[3], o_free[2];        // S A^T and V^T P^T are done; they are read
+    uint64_t end[2];
     uint32_t tmem;
     int abort;
     int scratch[34];
@@ -108,7 +109,7 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 // bounded number of times, until the phase completes or some role has given up
 // (at `abort`).  Called by whole warps; kept out of line, as every wait has one.
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t phase, uint32_t abort) {
-    for (uint32_t it = 0; it < (1u << 21); ++it) {
+    for (uint32_t it = 0; it < (1u << 18); ++it) {
         const bool ok = try_wait(bar, phase);
         if (__all_sync(0xffffffffu, ok)) return true;
         uint32_t stop;
@@ -130,6 +131,14 @@ __device__ __forceinline__ bool group_stop(int id, int threads, bool stop) {
         : "r"((uint32_t)stop), "r"(id), "r"(threads)
         : "memory");
     return any != 0;
+}
+
+__device__ __forceinline__ void load_tile(void *dst, const CUtensorMap *map, uint64_t *bar, int t0, int head) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(t0), "r"(0), "r"(head)
+        : "memory");
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -188,10 +197,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             mbar_init(&m->kv_free[b], kSThreads);
             mbar_init(&m->sc_full[b], 1);
             mbar_init(&m->p_full[b], kPThreads);
+            mbar_init(&m->o_free[b], kOThreads);
         }
         mbar_init(&m->s_full, kSThreads);
-        mbar_init(&m->o_free, kOThreads);
-        mbar_init(&m->end, 1);
+        mbar_init(&m->end[0], 1);
+        mbar_init(&m->end[1], 1);
         m->abort = 0;
         fence_barrier_init();
     }
@@ -219,9 +229,29 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         }
         return false;
     };
+    const uint64_t kmajor = sw128_kmajor_desc(sbase), mnmajor = sw128_mnmajor_desc(sbase, 8192, 1024);
     // block b in scan order: its first token and its tokens
     auto block_t0 = [&](int b) { return seg.t0 + (REV ? blocks - 1 - b : b) * C; };
     auto block_n = [&](int b) { return min(C, seg.len - (REV ? blocks - 1 - b : b) * C); };
+
+    auto load = [&](int b) {
+        if (elect_one()) {
+            const int ha = h / (p.H / p.HA), hb = h / (p.H / p.HB), hv = h / (p.H / p.HV);
+            uint64_t *bar = &m->full[b % Sh::NS];
+            uint8_t *st = sm + (b % Sh::NS) * Sh::STAGE;
+            const int t0 = block_t0(b);
+            mbar_arrive_expect_tx(bar, Sh::STAGE);
+            if (OUT) load_tile(st, &ma, bar, t0, ha);
+            load_tile(st + Sh::B_OFF, &mb, bar, t0, hb);
+            load_tile(st + Sh::V_OFF, &mv, bar, t0, hv);
+        }
+        __syncwarp();
+    };
+    // never leave a copy in flight into this CTA's shared memory
+    auto drain = [&](int issued) {
+        for (int b = issued > Sh::NS ? issued - Sh::NS : 0; b < issued; ++b)
+            (void)mbar_wait_sleep(&m->full[b % Sh::NS], (b / Sh::NS) & 1);
+    };
 
     if (warp >= 8) {
         // ------------------------------------------------ S: row r, 64 columns ----
@@ -373,7 +403,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                 tmem_wait_ld();
                 if (q == 3) {
                     tc_fence_before();
-                    arrive(BAR(o_free, 0));
+                    arrive(BAR(o_free, b & 1));
                 }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -393,21 +423,20 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                 }
             }
         }
-    } else if (warp == 3) {
-        // ------------------------------------------------------- MMA issuer ----
-        // The warp stays together and one elected lane issues, so that descriptors
-        // are uniform values: an operand's base, plus a constant for each step.
+    } else if (warp == 2) {
+        // ---------------------------------- issuer: scores and the state's update ----
+        // An issuing warp stays together and one elected lane issues, so that
+        // descriptors are uniform values: a base, plus a constant for each step.
         bool ok = true;
-        const uint64_t ka = sw128_kmajor_desc(sbase), mn = sw128_mnmajor_desc(sbase, 8192, 1024);
         auto scores = [&](int b) {
             const int s = b % Sh::NS;
             if (!(ok = warp_wait(BAR(full, s), b / Sh::NS, E_TMA))) return;
             if (block_n(b) < C && !(ok = warp_wait(BAR(w_full, b % Sh::NW), b / Sh::NW, E_HANDOFF))) return;
             // the buffer last held block b - 2's V^T P^T
-            if (b >= 2 && !(ok = warp_wait(BAR(o_free, 0), b - 2, E_HANDOFF))) return;
+            if (b >= 2 && !(ok = warp_wait(BAR(o_free, b & 1), (b - 2) >> 1, E_HANDOFF))) return;
             tc_fence_after();
             // rows 64 to 127 of A are what follows the tile: their scores are not read
-            const uint64_t at = ka + ((s * Sh::STAGE) >> 4);
+            const uint64_t at = kmajor + ((s * Sh::STAGE) >> 4);
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -420,15 +449,14 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         };
         if (OUT && blocks > 0) scores(0);
         for (int b = 0; b < blocks && ok; ++b) {
-            const int s = b % Sh::NS, w = b % Sh::NW;
-            const uint32_t st = (s * Sh::STAGE) >> 4;
-            const bool kv = b + 1 < blocks || want_state;
+            const int w = b % Sh::NW;
             if (!(ok = warp_wait(BAR(w_full, w), b / Sh::NW, E_HANDOFF))) break;
-            if (kv && b >= 2 && !(ok = warp_wait(BAR(kv_free, b & 1), (b >> 1) - 1, E_HANDOFF))) break;
-            tc_fence_after();
-            if (elect_one()) {
-                if (kv) {
-                    const uint64_t wd = mn + ((Sh::W_OFF + w * 3 * TILE) >> 4), bd = mn + (st + (Sh::B_OFF >> 4));
+            if (b + 1 < blocks || want_state) {
+                if (b >= 2 && !(ok = warp_wait(BAR(kv_free, b & 1), (b >> 1) - 1, E_HANDOFF))) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t wd = mnmajor + ((Sh::W_OFF + w * 3 * TILE) >> 4);
+                    const uint64_t bd = mnmajor + (((b % Sh::NS) * Sh::STAGE + Sh::B_OFF) >> 4);
                     const uint32_t d = tmem + T_KV + (b & 1) * D;
 #pragma unroll
                     for (int part = 2; part >= 0; --part)     // the small terms first
@@ -438,60 +466,64 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                                        part != 2 || k != 0);
                     mma_commit(&m->kv_full[b & 3]);
                 }
+                __syncwarp();
             }
-            __syncwarp();
-            if (!OUT) continue;
-            if (b + 1 < blocks) {
-                scores(b + 1);
-                if (!ok) break;
+            if (OUT && b + 1 < blocks) scores(b + 1);
+        }
+        // every MMA issued here is complete before TMEM is freed
+        if (elect_one()) mma_commit(&m->end[0]);
+        __syncwarp();
+        (void)mbar_wait_sleep(&m->end[0], 0);
+    } else if (warp == 3 && OUT) {
+        // ------------------------------------------- issuer: S A^T and V^T P^T ----
+        int issued = 0;
+        for (; issued < min(Sh::NS - 1, blocks); ++issued) load(issued);
+        for (int b = 0; b < blocks; ++b) {
+            // block b - 1 is done, and its state product, which the other issuer committed:
+            // its stage takes block b + 2 while S is on its way
+            if (b > 0 && !warp_wait(BAR(done, (b - 1) % 3), (b - 1) / 3, E_MMA)) break;
+            if (issued < blocks) {
+                if (b > 0 && !warp_wait(BAR(kv_full, (b - 1) & 3), (b - 1) >> 2, E_MMA)) break;
+                load(issued);
+                ++issued;
             }
-            if (!(ok = warp_wait(BAR(s_full, 0), b, E_HANDOFF))) break;
-            if (!(ok = warp_wait(BAR(p_full, b & 1), b >> 1, E_HANDOFF))) break;
-            if (b + 1 == blocks && b > 0 && !(ok = warp_wait(BAR(o_free, 0), b - 1, E_HANDOFF))) break;
+            if (!warp_wait(BAR(s_full, 0), b, E_HANDOFF)) break;
+            if (b > 0 && !warp_wait(BAR(o_free, (b - 1) & 1), (b - 1) >> 1, E_HANDOFF)) break;
             tc_fence_after();
+            const uint32_t st = ((b % Sh::NS) * Sh::STAGE) >> 4;
+            const uint64_t ad = kmajor + st, vd = mnmajor + (st + (Sh::V_OFF >> 4));
+            const uint64_t pd = kmajor + ((Sh::P_OFF + (b & 1) * 8192) >> 4);
             if (elect_one()) {
-                const uint64_t ad = ka + st, vd = mn + (st + (Sh::V_OFF >> 4));
-                const uint64_t pd = ka + ((Sh::P_OFF + (b & 1) * 8192) >> 4);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     mma_f16_ts(tmem + T_OI, tmem + T_SB + k * 8, ad + (((k >> 2) * 8192 + (k & 3) * 32) >> 4),
                                ID_N64, k != 0);
+            }
+            __syncwarp();
+            if (!warp_wait(BAR(p_full, b & 1), b >> 1, E_HANDOFF)) break;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     mma_f16_ss(tmem + T_X + (b & 1) * 64, vd + ((k * 2048) >> 4), pd + ((k * 32) >> 4), ID_PV, k != 0);
-                mma_commit(&m->done[s]);
+                mma_commit(&m->done[b % 3]);
             }
             __syncwarp();
         }
-        // every MMA issued here is complete before TMEM is freed
-        if (elect_one()) mma_commit(&m->end);
+        if (elect_one()) mma_commit(&m->end[1]);
         __syncwarp();
-        (void)mbar_wait_sleep(&m->end, 0);
-    } else if (warp == 2) {
-        // ------------------------------------------------------ tile loader ----
-        const int ha = h / (p.H / p.HA), hb = h / (p.H / p.HB), hv = h / (p.H / p.HV);
+        (void)mbar_wait_sleep(&m->end[1], 0);
+        drain(issued);
+    } else if (warp == 3) {
+        // ---------------------------------------- loader of the state's pass ----
         int issued = 0;
-        for (int b = 0; b < blocks; ++b) {
-            const int s = b % Sh::NS;
-            // a stage is free when the products that read it are done
-            if (b >= Sh::NS && !warp_wait(OUT ? BAR(done, s) : BAR(kv_full, s), b / Sh::NS - 1, E_MMA)) break;
-            if (elect_one()) {
-                uint8_t *st = sm + s * Sh::STAGE;
-                const int t0 = block_t0(b);
-                mbar_arrive_expect_tx(&m->full[s], Sh::STAGE);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (OUT) tma_load_3d(st + x * 8192, &ma, &m->full[s], x * 64, ha, t0);
-                    tma_load_3d(st + Sh::B_OFF + x * 8192, &mb, &m->full[s], x * 64, hb, t0);
-                    tma_load_3d(st + Sh::V_OFF + x * 8192, &mv, &m->full[s], x * 64, hv, t0);
-                }
-            }
-            __syncwarp();
-            issued = b + 1;
+        for (; issued < blocks; ++issued) {
+            // a stage is free when the product that reads it is done
+            const int f = issued - Sh::NS;
+            if (f >= 0 && !warp_wait(BAR(kv_full, f & 3), f >> 2, E_MMA)) break;
+            load(issued);
         }
-        // never leave a copy in flight into this CTA's shared memory
-        for (int b = issued > Sh::NS ? issued - Sh::NS : 0; b < issued; ++b)
-            (void)mbar_wait_sleep(&m->full[b % Sh::NS], (b / Sh::NS) & 1);
+        drain(issued);
     } else if (OUT) {
         // ------------------------------------------- P = scores .* decay, row i ----
         const int i = tid;
@@ -550,6 +582,20 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
     }
 }
 
+// [T, H, 128] bf16 seen as {64 channels, T, 2 halves, H}: one box is a tile of 64
+// tokens by 128 channels of one head, its halves one after the other.
+bool make_tile_map(CUtensorMap *map, const void *base, int total_T, int H) {
+    auto enc = get_encode();
+    if (enc == nullptr) return false;
+    cuuint64_t dims[4] = {64, (cuuint64_t)total_T, 2, (cuuint64_t)H};
+    cuuint64_t strides[3] = {(cuuint64_t)H * D * 2, 128, (cuuint64_t)D * 2};
+    cuuint32_t box[4] = {64, C, 2, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool OUT, bool REV, typename OutT>
 cudaError_t launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mv,
                    const ScanArgs &p, cudaStream_t stream) {
@@ -565,8 +611,8 @@ cudaError_t launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorM
 cudaError_t launch_scan_tc(const ScanArgs &p, bool reverse, bool states, bool out_f32,
                            cudaStream_t stream) {
     CUtensorMap ma, mb, mv;
-    if (!make_map(&ma, p.a, p.total_T, p.HA) || !make_map(&mb, p.b, p.total_T, p.HB) ||
-        !make_map(&mv, p.v, p.total_T, p.HV))
+    if (!make_tile_map(&ma, p.a, p.total_T, p.HA) || !make_tile_map(&mb, p.b, p.total_T, p.HB) ||
+        !make_tile_map(&mv, p.v, p.total_T, p.HV))
         return cudaErrorInvalidValue;
     if (states)
         return reverse ? launch<false, true, __nv_bfloat16>(ma, mb, mv, p, stream)
