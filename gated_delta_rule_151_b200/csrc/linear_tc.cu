@@ -141,6 +141,18 @@ __device__ __forceinline__ void load_tile(void *dst, const CUtensorMap *map, uin
         : "memory");
 }
 
+// 32 TMEM columns of 16 lanes: registers 4 k to 4 k + 3 hold columns 8 k + 2 (lane % 4)
+// and the next one of TMEM lane lane / 4, then of lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
@@ -258,28 +270,30 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         const int t = tid - kSThreads;
         const int r = (warp & 3) * 32 + lane, half = (warp - 8) >> 2;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-        float S[64];
+        float2 S[32];
         if (OUT && seg.index > 0) {   // states between segments lie in the order of these threads
             const float4 *src = reinterpret_cast<const float4 *>(
                 p.seg + ((size_t)(seg.state - 1) * p.H + h) * (D * D)) + t;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float4 x = src[i * kSThreads];
-                S[4 * i] = x.x; S[4 * i + 1] = x.y; S[4 * i + 2] = x.z; S[4 * i + 3] = x.w;
+                S[2 * i] = make_float2(x.x, x.y);
+                S[2 * i + 1] = make_float2(x.z, x.w);
             }
         } else if (seg.index > 0 || p.s_in == nullptr) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) S[i] = 0.f;
+            for (int i = 0; i < 32; ++i) S[i] = make_float2(0.f, 0.f);
         } else if (p.turned) {
             const float *src = p.s_in + state_at + (size_t)half * 64 * D + r;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) S[i] = src[i * D];
+            for (int i = 0; i < 32; ++i) S[i] = make_float2(src[2 * i * D], src[(2 * i + 1) * D]);
         } else {
             const float4 *src = reinterpret_cast<const float4 *>(p.s_in + state_at + r * D + half * 64);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float4 x = src[i];
-                S[4 * i] = x.x; S[4 * i + 1] = x.y; S[4 * i + 2] = x.z; S[4 * i + 3] = x.w;
+                S[2 * i] = make_float2(x.x, x.y);
+                S[2 * i + 1] = make_float2(x.z, x.w);
             }
         }
         bool ok = true;
@@ -300,7 +314,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             }
             if (b + 1 < blocks || want_state) {
                 uint8_t *wbuf = sm + Sh::W_OFF + w * 3 * TILE;
-#pragma unroll
+#pragma unroll 2
                 for (int u = 0; u < 4; ++u) {
                     const uint32_t at = (uint32_t)(u * kSThreads + t) * 16;   // swizzled place: row in bits 7-12
                     const int j = (at >> 7) & 63;
@@ -334,7 +348,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                 tc_fence_after();
                 uint32_t x[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = pack_bf16(S[2 * i], S[2 * i + 1]);
+                for (int i = 0; i < 32; ++i) x[i] = pack_bf16(S[i].x, S[i].y);
                 tmem_st32(tmem + lanes + T_SB + half * 32, x);
                 tmem_wait_st();
                 tc_fence_before();
@@ -354,7 +368,9 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                 tmem_ld16(tmem + lanes + T_KV + (b & 1) * D + half * 64 + q * 16, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[q * 16 + i] = fmaf(gn, S[q * 16 + i], __uint_as_float(x[i]));
+                for (int i = 0; i < 8; ++i)
+                    S[q * 8 + i] = __ffma2_rn(make_float2(gn, gn), S[q * 8 + i],
+                                              make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])));
             }
             tc_fence_before();
             arrive(BAR(kv_free, b & 1));
@@ -364,62 +380,88 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                 float4 *dst = reinterpret_cast<float4 *>(p.s_out + state_at + r * D + half * 64);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    dst[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+                    dst[i] = make_float4(S[2 * i].x, S[2 * i].y, S[2 * i + 1].x, S[2 * i + 1].y);
             }
         } else {
             float4 *dst = reinterpret_cast<float4 *>(seg_out) + t;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                dst[i * kSThreads] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+                dst[i * kSThreads] = make_float4(S[2 * i].x, S[2 * i].y, S[2 * i + 1].x, S[2 * i + 1].y);
         }
     } else if (warp >= 4) {
-        // --------------------------------------- O: value channel r, all tokens ----
-        const int r = tid - 128;
+        // ------------------------------------------ O: 32 channels a warp, all tokens ----
+        // TMEM comes in as fragments: a thread has the tokens 8 k + 2 (lane % 4) and the next
+        // one of the channels lane / 4 + {0, 8} of each 16, which stmatrix turns into rows of
+        // the tile [token][channel] (16-byte pieces swapped by token % 8 against conflicts).
+        const int t = tid - 128;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const size_t row = (size_t)p.H * D;
-        OutT *tile = reinterpret_cast<OutT *>(sm + Sh::O_OFF) + r;
+        float2 lead[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) lead[k] = *reinterpret_cast<const float2 *>(m->lead + 8 * k + 2 * (lane & 3));
         for (int b = 0; OUT && b < blocks; ++b) {
-            constexpr bool kTile = sizeof(OutT) == 2;
             const bool ok = warp_wait(BAR(done, b % 3), b / 3, E_MMA);
-            // bf16 goes through a tile and leaves 16 bytes a thread: 2-byte stores from
-            // the lanes' channels took 3,400 cycles a block, one bulk copy a row 2,600
             if (group_stop(1, kOThreads, !ok)) break;   // (and the last tile has left)
             tc_fence_after();
             const int n = block_n(b);
             OutT *dst = static_cast<OutT *>(p.out) + ((size_t)block_t0(b) * p.H + h) * D;
+            if (REV && (n < C || b == 1)) {             // lead counts from the block's last token
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t xi[16], xa[16];
-                float lead[16];
-                tmem_ld16(tmem + lanes + T_OI + q * 16, xi);
-                tmem_ld16(tmem + lanes + T_X + (b & 1) * 64 + q * 16, xa);
-#pragma unroll
-                for (int e = 0; e < 16; e += 4)
-                    *reinterpret_cast<float4 *>(lead + e) = *reinterpret_cast<const float4 *>(m->lead + q * 16 + e);
-                if (REV && n < C) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) lead[e] = m->pw[max(n - 1 - (q * 16 + e), 0)];
-                }
-                tmem_wait_ld();
-                if (q == 3) {
-                    tc_fence_before();
-                    arrive(BAR(o_free, b & 1));
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int i = q * 16 + e;
-                    const float o = fmaf(lead[e], __uint_as_float(xi[e]), __uint_as_float(xa[e]));
-                    if (kTile) store_io(tile + i * D, o);
-                    else if (i < n) store_io(dst + i * row + r, o);
+                for (int k = 0; k < 8; ++k) {
+                    const int i = 8 * k + 2 * (lane & 3);
+                    lead[k] = make_float2(m->pw[max(n - 1 - i, 0)], m->pw[max(n - 2 - i, 0)]);
                 }
             }
-            if (kTile) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {               // channels 32 (warp % 4) + 16 c ..
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {  // tokens 32 half ..
+                    uint32_t xi[16], xa[16];
+                    const uint32_t from = tmem + lanes + ((uint32_t)c << 20) + half * 32;
+                    tmem_ld_frag(from + T_OI, xi);
+                    tmem_ld_frag(from + T_X + (b & 1) * 64, xa);
+                    tmem_wait_ld();
+                    if (c == 1 && half == 1) {
+                        tc_fence_before();
+                        arrive(BAR(o_free, b & 1));
+                    }
+                    const int ch = 32 * (warp & 3) + 16 * c;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 w = lead[half * 4 + k];
+                        const float2 top = __ffma2_rn(w, make_float2(__uint_as_float(xi[4 * k]), __uint_as_float(xi[4 * k + 1])),
+                                                      make_float2(__uint_as_float(xa[4 * k]), __uint_as_float(xa[4 * k + 1])));
+                        const float2 low = __ffma2_rn(w, make_float2(__uint_as_float(xi[4 * k + 2]), __uint_as_float(xi[4 * k + 3])),
+                                                      make_float2(__uint_as_float(xa[4 * k + 2]), __uint_as_float(xa[4 * k + 3])));
+                        const int i = half * 32 + 8 * k;
+                        if constexpr (sizeof(OutT) == 2) {
+                            // matrices: channels ch + {0, 8}; lane l gives the place of token i + l % 8
+                            const uint32_t at = sbase + Sh::O_OFF + (i + (lane & 7)) * 256 +
+                                                ((((ch >> 3) + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+                            asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(at),
+                                         "r"(pack_bf16(top.x, top.y)), "r"(pack_bf16(low.x, low.y))
+                                         : "memory");
+                        } else {
+                            const int i0 = i + 2 * (lane & 3), c0 = ch + (lane >> 2);
+                            if (i0 < n) {
+                                store_io(dst + i0 * row + c0, top.x);
+                                store_io(dst + i0 * row + c0 + 8, low.x);
+                            }
+                            if (i0 + 1 < n) {
+                                store_io(dst + (i0 + 1) * row + c0, top.y);
+                                store_io(dst + (i0 + 1) * row + c0 + 8, low.y);
+                            }
+                        }
+                    }
+                }
+            }
+            if constexpr (sizeof(OutT) == 2) {
                 if (group_stop(1, kOThreads, false)) break;
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    const int e = u * kOThreads + r, i = e >> 4;
-                    const uint4 x = *reinterpret_cast<const uint4 *>(sm + Sh::O_OFF + e * 16);
-                    if (i < n) *reinterpret_cast<uint4 *>(dst + i * row + (e & 15) * 8) = x;
+                    const int e = u * kOThreads + t, i = e >> 4, piece = e & 15;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(sm + Sh::O_OFF + i * 256 + ((piece ^ (i & 7)) << 4));
+                    if (i < n) *reinterpret_cast<uint4 *>(dst + i * row + piece * 8) = x;
                 }
             }
         }
@@ -487,6 +529,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                 load(issued);
                 ++issued;
             }
+            if (!warp_wait(BAR(full, b % Sh::NS), b / Sh::NS, E_TMA)) break;
             if (!warp_wait(BAR(s_full, 0), b, E_HANDOFF)) break;
             if (b > 0 && !warp_wait(BAR(o_free, (b - 1) & 1), (b - 1) >> 1, E_HANDOFF)) break;
             tc_fence_after();
@@ -528,15 +571,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         // ------------------------------------------- P = scores .* decay, row i ----
         const int i = tid;
         const uint32_t lanes = (uint32_t)warp << 21;
-        // with i = 8 I + f, j = 8 J + e: x^|i-j| = x^{8|I-J|} x^{|f-e|} where e lies on f's
-        // causal side, else x^{8(|I-J|-1)} x^{8-|f-e|}: sixteen factors a thread, two a group
-        const int I = i >> 3, f = i & 7;
-        float near[8], far[8];
+        float2 decay[32];            // row i of M
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int apart = REV ? e - f : f - e;
-            near[e] = apart >= 0 ? m->pw[apart] : 0.f;
-            far[e] = apart < 0 ? m->pw[8 + apart] : 0.f;
+        for (int j = 0; j < C; j += 2) {
+            const int a0 = REV ? j - i : i - j, a1 = REV ? j + 1 - i : i - j - 1;
+            decay[j / 2] = make_float2(a0 >= 0 ? m->pw[max(a0, 0)] : 0.f, a1 >= 0 ? m->pw[max(a1, 0)] : 0.f);
         }
         for (int b = 0; b < blocks; ++b) {
             if (!warp_wait(BAR(sc_full, b & 1), b >> 1, E_MMA)) break;
@@ -546,27 +585,31 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             const uint32_t dst = sbase + Sh::P_OFF + (b & 1) * 8192;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
+                // 32 columns: this warp's rows lie on the diagonal, all after, or all before them
+                const bool diagonal = half == warp || (REV && n < C);
+                const bool none = !diagonal && (REV ? half < warp : half > warp);
                 uint32_t x[32];
-                tmem_ld32(tmem + lanes + T_X + (b & 1) * 64 + half * 32, x);
-                tmem_wait_ld();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int J = half * 4 + q, G = REV ? J - I : I - J;
-                    const float g0 = G >= 0 ? m->pw[8 * max(G, 0)] : 0.f;
-                    const float g1 = G >= 1 ? m->pw[8 * max(G - 1, 0)] : 0.f;
-                    const float2 m0 = make_float2(g0, g0), m1 = make_float2(g1, g1);
-                    uint32_t y[4];
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const float2 w = __ffma2_rn(make_float2(far[e], far[e + 1]), m1,
-                                                    __fmul2_rn(make_float2(near[e], near[e + 1]), m0));
-                        const float2 s = __fmul2_rn(make_float2(__uint_as_float(x[q * 8 + e]), __uint_as_float(x[q * 8 + e + 1])), w);
-                        const int j = J * 8 + e;     // masked by selection: a score may be anything there
-                        y[e >> 1] = pack_bf16((REV ? j >= i && j < n : j <= i) ? s.x : 0.f,
-                                              (REV ? j + 1 >= i && j + 1 < n : j + 1 <= i) ? s.y : 0.f);
-                    }
-                    st_shared_v4(dst + sw128_offset(i, J), y[0], y[1], y[2], y[3]);
+                if (!none) {
+                    tmem_ld32(tmem + lanes + T_X + (b & 1) * 64 + half * 32, x);
+                    tmem_wait_ld();
                 }
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const int j = half * 32 + e;
+                    uint32_t y = 0;
+                    if (!none) {
+                        float2 s = __fmul2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), decay[j / 2]);
+                        if (diagonal) {      // masked by selection: a score may be anything there
+                            s.x = (REV ? j >= i && j < n : j <= i) ? s.x : 0.f;
+                            s.y = (REV ? j + 1 >= i && j + 1 < n : j + 1 <= i) ? s.y : 0.f;
+                        }
+                        y = pack_bf16(s.x, s.y);
+                    }
+                    x[e / 2] = y;
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    st_shared_v4(dst + sw128_offset(i, half * 4 + q), x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
             }
             tc_fence_before();
             fence_proxy_async();

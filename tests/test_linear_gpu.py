@@ -154,7 +154,7 @@ def test_decode_continues_prefill():
     ref.check("state", fin, want[2], want[3])
 
 
-@pytest.mark.parametrize("T", [100, 4097])
+@pytest.mark.parametrize("T", [100, 4097, 20000])
 def test_state_in_place_and_repeatable(T):
     _, x = make(T, 2, 2, 128, 128, torch.bfloat16, 1, None, True, seed=7)
     o1, s1 = gdr.gdr_linear_prefill(x["q"], x["k"], x["v"], x["decay"], x["state"])
