@@ -26,6 +26,7 @@
 // wait for S and P; 4-7 write O; 8-15 hold S, 64 columns of one row a thread, and
 // split the weighted V.  The pass that only wants the state uses 2, 3 and 8-15.
 #include <cstddef>
+#include <type_traits>
 
 #include "chunk_common.cuh"
 #include "linear_common.cuh"
@@ -41,19 +42,21 @@ constexpr uint32_t TILE = 16384;            // 64 tokens x 128 channels bf16, tw
 template <bool OUT>
 struct Shape {
     static constexpr int NS = OUT ? 3 : 4;                   // tiles in the ring
-    static constexpr int NW = OUT ? 1 : 2;                   // buffers of the split V
+    static constexpr int NB = OUT ? 1 : 2;                   // buffers of the split V and of its product
     static constexpr uint32_t STAGE = (OUT ? 3 : 2) * TILE;
     static constexpr uint32_t B_OFF = OUT ? TILE : 0;        // A, B, V in a stage
     static constexpr uint32_t V_OFF = B_OFF + TILE;
-    static constexpr uint32_t W_OFF = NS * STAGE;            // high, middle, low part
-    static constexpr uint32_t P_OFF = W_OFF + NW * 3 * TILE; // two buffers of 64 x 64 bf16
+    static constexpr uint32_t P_OFF = NS * STAGE;            // two buffers of 64 x 64 bf16
     static constexpr uint32_t O_OFF = P_OFF + (OUT ? 2 * 8192 : 0);   // a tile of O on its way out
     static constexpr uint32_t MISC = O_OFF + (OUT ? TILE : 0);
+    // TMEM columns
+    static constexpr uint32_t T_KV = 0;                      // NB of 128: (diag(w) V)^T B
+    static constexpr uint32_t T_W = NB * 128;                // NB of 96: (diag(w) V)^T, its high, middle, low part
 };
 
 struct Misc {
     uint64_t full[4];                   // a stage's tiles have arrived
-    uint64_t w_full[2];                 // the split V is written
+    uint64_t w_full[4];                 // half of the split V is written
     uint64_t kv_full[4], kv_free[2];    // its product is done (and its buffer free), and read
     uint64_t sc_full[2], p_full[2];     // scores are done; P is written
     uint64_t s_full;                    // S in bf16 is written
@@ -71,8 +74,6 @@ template <bool OUT>
 constexpr int smem_bytes() { return (int)(Shape<OUT>::MISC + sizeof(Misc)); }
 static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "shared memory");
 
-// TMEM columns
-constexpr uint32_t T_KV = 0;        // two buffers of 128
 constexpr uint32_t T_X = 256;       // two buffers of 64: a block's scores, then its V^T P^T
 constexpr uint32_t T_OI = 384;      // S A^T
 constexpr uint32_t T_SB = 448;      // S in bf16
@@ -80,7 +81,7 @@ constexpr uint32_t T_COLS = 512;
 
 constexpr uint32_t ID_N64 = make_idesc(1, 128, 64);
 constexpr uint32_t ID_PV = ID_N64 | kIdescAMN;
-constexpr uint32_t ID_KV = make_idesc(1, 128, 128) | kIdescAMN | kIdescBMN;
+constexpr uint32_t ID_KV = make_idesc(1, 128, 128) | kIdescBMN;
 
 enum : uint32_t { E_ALIGN = 1, E_TMA = 2, E_MMA = 4, E_HANDOFF = 8 };
 
@@ -153,6 +154,14 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) 
         : "r"(taddr));
 }
 
+// The same fragment of 16 lanes by 8 columns of 32 bits to TMEM: registers 2 k and 2 k + 1
+// go to column 4 k + lane % 4 of TMEM lanes lane / 4 and lane / 4 + 8.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
@@ -206,6 +215,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         for (int s = 0; s < 3; ++s) mbar_init(&m->done[s], 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&m->w_full[b], kSThreads);
+            mbar_init(&m->w_full[2 + b], kSThreads);
             mbar_init(&m->kv_free[b], kSThreads);
             mbar_init(&m->sc_full[b], 1);
             mbar_init(&m->p_full[b], kPThreads);
@@ -297,49 +307,82 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             }
         }
         bool ok = true;
-        // diag(w) V of block b in three bf16 parts, in the tile's own layout
+        // (diag(w) V)^T of block b in three bf16 parts to TMEM, the product's other operand:
+        // 32 tokens, then the other 32, whose split the first ones' product hides.  A warp
+        // takes 32 channels (its lanes) by 16 of the tokens.  ldmatrix hands a thread tokens
+        // 8 m + 2 (lane % 4) and the next one of channels lane / 4 + {0, 8}, the fragment that
+        // tcgen05.st writes; through shared memory the parts cost 96 KB of its 336 KB of
+        // traffic a block, which was the bound.
+        float2 weight[4];
+        auto weights = [&](int n) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = (k >> 1) * 32 + half * 16 + (k & 1) * 8 + 2 * (lane & 3);
+                weight[k] = make_float2(m->pw[REV ? j + 1 : max(n - 1 - j, 0)], m->pw[REV ? j + 2 : max(n - 2 - j, 0)]);
+            }
+        };
+        weights(C);
         auto split_v = [&](int b) {
-            const int s = b % Sh::NS, w = b % Sh::NW, n = block_n(b);
+            const int s = b % Sh::NS, n = block_n(b);
             if (!(ok = warp_wait(BAR(full, s), b / Sh::NS, E_TMA))) return;
-            if (b >= Sh::NW && !(ok = warp_wait(BAR(kv_full, (b - Sh::NW) & 3), (b - Sh::NW) >> 2, E_MMA))) return;
-            uint8_t *stage = sm + s * Sh::STAGE;
+            const uint32_t stage = sbase + s * Sh::STAGE;
             // rows behind the segment's last token hold another sequence's tokens (or
             // anything): they leave B and V, since 0 * inf is not 0
             if (n < C) {
                 for (int e = t; e < 2 * (C - n) * 8; e += kSThreads) {
                     const uint32_t at = (e & 1) * 8192 + (n + (e >> 4)) * 128 + ((e >> 1) & 7) * 16;
-                    *reinterpret_cast<uint4 *>(stage + Sh::B_OFF + at) = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4 *>(stage + Sh::V_OFF + at) = make_uint4(0, 0, 0, 0);
+                    st_shared_v4(stage + Sh::B_OFF + at, 0, 0, 0, 0);
+                    st_shared_v4(stage + Sh::V_OFF + at, 0, 0, 0, 0);
                 }
+                fence_proxy_async();
+                if (!REV) weights(n);
             }
-            if (b + 1 < blocks || want_state) {
-                uint8_t *wbuf = sm + Sh::W_OFF + w * 3 * TILE;
-#pragma unroll 2
-                for (int u = 0; u < 4; ++u) {
-                    const uint32_t at = (uint32_t)(u * kSThreads + t) * 16;   // swizzled place: row in bits 7-12
-                    const int j = (at >> 7) & 63;
-                    const float wj = m->pw[REV ? j + 1 : max(n - 1 - j, 0)];
-                    const float2 w2 = make_float2(wj, wj), minus = make_float2(-1.f, -1.f);
-                    uint4 x = *reinterpret_cast<const uint4 *>(stage + Sh::V_OFF + at);
-                    if (j >= n) x = make_uint4(0, 0, 0, 0);
-                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t hi[4], mid[4], lo[4];
+            // (the product that last read this buffer was waited for by its update of S)
+            tc_fence_after();
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float2 f = __fmul2_rn(make_float2(bf16_lo(in[e]), bf16_hi(in[e])), w2);
+            for (int h2 = 0; h2 < 2; ++h2) {
+                if (b + 1 < blocks || want_state) {
+                    const int j0 = h2 * 32 + half * 16;
+                    uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {      // 16 channels
+                        const int ch = (warp & 3) * 32 + c * 16 + (lane & 8);
+                        const int j = j0 + (lane & 7) + ((lane >> 4) << 3);
+                        const uint32_t at = stage + Sh::V_OFF + (ch >> 6) * 8192 + sw128_offset(j, (ch >> 3) & 7);
+                        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(hi[4 * c]), "=r"(hi[4 * c + 1]), "=r"(hi[4 * c + 2]), "=r"(hi[4 * c + 3])
+                                     : "r"(at)
+                                     : "memory");
+                    }
+                    if (n < C) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int j = j0 + ((e >> 1) & 1) * 8 + 2 * (lane & 3);
+                            hi[e] = j + 1 < n ? hi[e] : j < n ? hi[e] & 0xffffu : 0u;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 minus = make_float2(-1.f, -1.f);
+                        float2 f = __fmul2_rn(make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])), weight[h2 * 2 + ((e >> 1) & 1)]);
                         hi[e] = pack_bf16(f.x, f.y);
                         f = __ffma2_rn(make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])), minus, f);
                         mid[e] = pack_bf16(f.x, f.y);
                         f = __ffma2_rn(make_float2(bf16_lo(mid[e]), bf16_hi(mid[e])), minus, f);
                         lo[e] = pack_bf16(f.x, f.y);
                     }
-                    *reinterpret_cast<uint4 *>(wbuf + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(wbuf + TILE + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                    *reinterpret_cast<uint4 *>(wbuf + 2 * TILE + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    const uint32_t to = tmem + lanes + Sh::T_W + (b % Sh::NB) * 96 + j0 / 2;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        tmem_st_frag(to + (c << 20), hi + 4 * c);
+                        tmem_st_frag(to + (c << 20) + 32, mid + 4 * c);
+                        tmem_st_frag(to + (c << 20) + 64, lo + 4 * c);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
                 }
+                arrive(BAR(w_full, (b % Sh::NB) * 2 + h2));
             }
-            fence_proxy_async();
-            arrive(BAR(w_full, w));
         };
         if (blocks > 0) split_v(0);
         for (int b = 0; b < blocks && ok; ++b) {
@@ -354,7 +397,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                 tc_fence_before();
                 arrive(BAR(s_full, 0));
             }
-            if (b + 1 < blocks) {
+            if (!OUT && b + 1 < blocks) {       // two buffers: the next split goes ahead of this update
                 split_v(b + 1);
                 if (!ok) break;
             }
@@ -365,7 +408,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint32_t x[16];
-                tmem_ld16(tmem + lanes + T_KV + (b & 1) * D + half * 64 + q * 16, x);
+                tmem_ld16(tmem + lanes + Sh::T_KV + (b % Sh::NB) * D + half * 64 + q * 16, x);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -373,7 +416,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                                               make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])));
             }
             tc_fence_before();
-            arrive(BAR(kv_free, b & 1));
+            arrive(BAR(kv_free, b % Sh::NB));
+            if (OUT && b + 1 < blocks) split_v(b + 1);
         }
         if (OUT) {
             if (want_state) {
@@ -473,7 +517,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         auto scores = [&](int b) {
             const int s = b % Sh::NS;
             if (!(ok = warp_wait(BAR(full, s), b / Sh::NS, E_TMA))) return;
-            if (block_n(b) < C && !(ok = warp_wait(BAR(w_full, b % Sh::NW), b / Sh::NW, E_HANDOFF))) return;
+            if (block_n(b) < C && !(ok = warp_wait(BAR(w_full, (b % Sh::NB) * 2), b / Sh::NB, E_HANDOFF))) return;
             // the buffer last held block b - 2's V^T P^T
             if (b >= 2 && !(ok = warp_wait(BAR(o_free, b & 1), (b - 2) >> 1, E_HANDOFF))) return;
             tc_fence_after();
@@ -491,25 +535,26 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         };
         if (OUT && blocks > 0) scores(0);
         for (int b = 0; b < blocks && ok; ++b) {
-            const int w = b % Sh::NW;
-            if (!(ok = warp_wait(BAR(w_full, w), b / Sh::NW, E_HANDOFF))) break;
-            if (b + 1 < blocks || want_state) {
-                if (b >= 2 && !(ok = warp_wait(BAR(kv_free, b & 1), (b >> 1) - 1, E_HANDOFF))) break;
+            const int w = b % Sh::NB;
+            const bool kv = b + 1 < blocks || want_state;
+            if (kv && b >= Sh::NB && !(ok = warp_wait(BAR(kv_free, w), b / Sh::NB - 1, E_HANDOFF))) break;
+            const uint64_t bd = mnmajor + (((b % Sh::NS) * Sh::STAGE + Sh::B_OFF) >> 4);
+            const uint32_t d = tmem + Sh::T_KV + w * D, a = tmem + Sh::T_W + w * 96;
+#pragma unroll
+            for (int h2 = 0; h2 < 2; ++h2) {
+                if (ok) ok = warp_wait(BAR(w_full, w * 2 + h2), b / Sh::NB, E_HANDOFF);
                 tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t wd = mnmajor + ((Sh::W_OFF + w * 3 * TILE) >> 4);
-                    const uint64_t bd = mnmajor + (((b % Sh::NS) * Sh::STAGE + Sh::B_OFF) >> 4);
-                    const uint32_t d = tmem + T_KV + (b & 1) * D;
+                if (ok && kv && elect_one()) {
 #pragma unroll
                     for (int part = 2; part >= 0; --part)     // the small terms first
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f16_ss(d, wd + ((part * TILE + k * 2048) >> 4), bd + ((k * 2048) >> 4), ID_KV,
-                                       part != 2 || k != 0);
-                    mma_commit(&m->kv_full[b & 3]);
+                        for (int k = 2 * h2; k < 2 * h2 + 2; ++k)
+                            mma_f16_ts(d, a + part * 32 + k * 8, bd + ((k * 2048) >> 4), ID_KV, part != 2 || k != 0);
+                    if (h2 == 1) mma_commit(&m->kv_full[b & 3]);
                 }
                 __syncwarp();
             }
+            if (!ok) break;
             if (OUT && b + 1 < blocks) scores(b + 1);
         }
         // every MMA issued here is complete before TMEM is freed
@@ -583,34 +628,41 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             tc_fence_after();
             const int n = block_n(b);
             const uint32_t dst = sbase + Sh::P_OFF + (b & 1) * 8192;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                // 32 columns: this warp's rows lie on the diagonal, all after, or all before them
-                const bool diagonal = half == warp || (REV && n < C);
-                const bool none = !diagonal && (REV ? half < warp : half > warp);
+            // 32 columns at a time: they lie on the diagonal of this warp's rows, all on their
+            // causal side, or all on the other
+            auto columns = [&](auto which) {
+                constexpr int half = decltype(which)::value;
+                const uint32_t at = tmem + lanes + T_X + (b & 1) * 64 + half * 32;
                 uint32_t x[32];
-                if (!none) {
-                    tmem_ld32(tmem + lanes + T_X + (b & 1) * 64 + half * 32, x);
+                if (half == warp || (REV && n < C)) {
+                    tmem_ld32(at, x);
                     tmem_wait_ld();
-                }
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const int j = half * 32 + e;
-                    uint32_t y = 0;
-                    if (!none) {
-                        float2 s = __fmul2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), decay[j / 2]);
-                        if (diagonal) {      // masked by selection: a score may be anything there
-                            s.x = (REV ? j >= i && j < n : j <= i) ? s.x : 0.f;
-                            s.y = (REV ? j + 1 >= i && j + 1 < n : j + 1 <= i) ? s.y : 0.f;
-                        }
-                        y = pack_bf16(s.x, s.y);
+                    for (int e = 0; e < 32; e += 2) {    // masked by selection: a score may be anything there
+                        const int j = half * 32 + e;
+                        const float2 s = __fmul2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), decay[j / 2]);
+                        x[e / 2] = pack_bf16((REV ? j >= i && j < n : j <= i) ? s.x : 0.f,
+                                             (REV ? j + 1 >= i && j + 1 < n : j + 1 <= i) ? s.y : 0.f);
                     }
-                    x[e / 2] = y;
+                } else if (REV ? half < warp : half > warp) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = 0;
+                } else {
+                    tmem_ld32(at, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 s = __fmul2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                                    decay[(half * 32 + e) / 2]);
+                        x[e / 2] = pack_bf16(s.x, s.y);
+                    }
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     st_shared_v4(dst + sw128_offset(i, half * 4 + q), x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-            }
+            };
+            columns(std::integral_constant<int, 0>{});
+            columns(std::integral_constant<int, 1>{});
             tc_fence_before();
             fence_proxy_async();
             arrive(BAR(p_full, b & 1));
