@@ -119,6 +119,7 @@ struct Call {
     bool bf16;
     cudaStream_t stream;
     uint32_t used;   // status words handed out
+    bool launched;   // a kernel of this call went before
 
     cudaError_t scan(const void *a, int HA, const void *b, int HB, const void *v, int HV, int d_b,
                      int d_v, const float *s_in, bool turned, float *s_out, void *out, bool out_f32,
@@ -143,7 +144,9 @@ struct Call {
         cudaError_t e = cudaSuccess;
         if (plan.inner > 0) {
             e = pass(p, d_b, d_v, reverse, true, out_f32);
-            if (e == cudaSuccess) e = launch_scan_join(p, d_b * d_v, reverse, stream);
+            // (of two segments the first one's own state is what the second starts from)
+            if (e == cudaSuccess && (cu != nullptr || plan.inner > N))
+                e = launch_scan_join(p, d_b * d_v, reverse, stream);
             p.status += (size_t)plan.inner * H;
         }
         if (e == cudaSuccess) e = pass(p, d_b, d_v, reverse, false, out_f32);
@@ -152,8 +155,10 @@ struct Call {
     }
 
     cudaError_t pass(const ScanArgs &p, int d_b, int d_v, bool reverse, bool states, bool out_f32) {
-        if (tensor_cores(d_b, d_v, bf16)) return launch_scan_tc(p, reverse, states, out_f32, stream);
-        return launch_scan_simt(p, d_b, d_v, reverse, states, bf16, out_f32, stream);
+        const bool after = launched;
+        launched = true;
+        if (tensor_cores(d_b, d_v, bf16)) return launch_scan_tc(p, reverse, states, out_f32, after, stream);
+        return launch_scan_simt(p, d_b, d_v, reverse, states, bf16, out_f32, after, stream);
     }
 };
 
@@ -227,7 +232,7 @@ gdr_status_t gdr_linear_prefill(const void *q, const void *k, const void *v, con
     if (total_T == 0) return status_of(pass_state(final_state, initial_state, state, s));
 
     Call c{cu_seqlens, decay, num_seqs, total_T, H, plan, lay, static_cast<uint8_t *>(workspace),
-           io_dtype == GDR_BF16, s, 0};
+           io_dtype == GDR_BF16, s, 0, false};
     // in place and in segments: the last segment of a sequence may end before its
     // first one has read the incoming state, which therefore moves aside
     if (initial_state != nullptr && initial_state == final_state && plan.inner > 0) {
@@ -311,7 +316,7 @@ gdr_status_t gdr_linear_backward(const void *q, const void *k, const void *v, co
     if (total_T == 0) return status_of(pass_state(d_initial_state, d_final_state, state, s));
 
     Call c{cu_seqlens, decay, num_seqs, total_T, H, plan, lay, static_cast<uint8_t *>(workspace),
-           io_dtype == GDR_BF16, s, 0};
+           io_dtype == GDR_BF16, s, 0, false};
     // heads that share a query/key head: each one's dq and dk in fp32, then their sum
     const int group = H / H_qk;
     float *part = reinterpret_cast<float *>(c.ws + lay.part);

@@ -133,15 +133,39 @@ __device__ inline Segment find_segment(const ScanArgs &p, int slot, bool inner, 
     return s;
 }
 
+// The kernels of one call follow each other without draining the GPU between them:
+// each lets the next one start once its own blocks have, and waits for the one
+// before to be complete where it first touches memory that passes between them.
+// Every kernel launched with `after` waits in every block that has work, so a
+// kernel is complete only when all before it in the call are.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... Params, typename... Args>
+cudaError_t launch_kernel(bool after, void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                          cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    cudaLaunchAttribute a = {};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &a;
+    c.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&c, kernel, Params(args)...);
+}
+
 // Launchers.  `states`: the pass that writes the segments' own states (all but
 // each sequence's last segment in scan order); otherwise the output pass.
-cudaError_t launch_scan_tc(const ScanArgs &p, bool reverse, bool states, bool out_f32,
+cudaError_t launch_scan_tc(const ScanArgs &p, bool reverse, bool states, bool out_f32, bool after,
                            cudaStream_t stream);   // bf16, d_b = d_v = 128
 cudaError_t launch_scan_simt(const ScanArgs &p, int d_b, int d_v, bool reverse, bool states,
-                             bool bf16, bool out_f32, cudaStream_t stream);
-// Segments' own states -> states behind each segment, in place.
+                             bool bf16, bool out_f32, bool after, cudaStream_t stream);
+// Segments' own states -> states behind each segment, in place (after the states' pass).
 cudaError_t launch_scan_join(const ScanArgs &p, int elements, bool reverse, cudaStream_t stream);
-// [T, H, d] fp32 partial gradients summed over each group of H / H_qk heads.
+// [T, H, d] fp32 partial gradients summed over each group of H / H_qk heads (after a pass).
 cudaError_t launch_group_sum(const float *part, int64_t T, int H_qk, int group, int d, bool bf16,
                              void *out, cudaStream_t stream);
 cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, const float *decay,

@@ -34,6 +34,8 @@ scan_simt_kernel(const ScanArgs p) {
     __shared__ int scratch[34];
     const int tid = threadIdx.x;
     const int slot = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    launch_dependents();
+    wait_for_previous();
     if (OUT && blockIdx.x == 0 && tid == 0) *p.header = p.status_words;
     const Segment seg = find_segment(p, slot, !OUT, REV, scratch, NT);
     if (seg.n < 0) return;
@@ -150,39 +152,36 @@ scan_simt_kernel(const ScanArgs p) {
 }
 
 template <int DB, int DV, typename In, typename Out>
-cudaError_t launch_shape(const ScanArgs &p, bool reverse, bool states, cudaStream_t stream) {
+cudaError_t launch_shape(const ScanArgs &p, bool reverse, bool states, bool after, cudaStream_t s) {
     constexpr int NT = DV < 32 ? 32 : DV;
     const unsigned grid = (unsigned)(states ? p.inner : p.slots) * p.H;
-    if (states) {
-        if (reverse) scan_simt_kernel<DB, DV, false, true, In, In><<<grid, NT, 0, stream>>>(p);
-        else scan_simt_kernel<DB, DV, false, false, In, In><<<grid, NT, 0, stream>>>(p);
-    } else {
-        if (reverse) scan_simt_kernel<DB, DV, true, true, In, Out><<<grid, NT, 0, stream>>>(p);
-        else scan_simt_kernel<DB, DV, true, false, In, Out><<<grid, NT, 0, stream>>>(p);
-    }
-    return cudaGetLastError();
+    if (states)
+        return reverse ? launch_kernel(after, scan_simt_kernel<DB, DV, false, true, In, In>, grid, NT, 0, s, p)
+                       : launch_kernel(after, scan_simt_kernel<DB, DV, false, false, In, In>, grid, NT, 0, s, p);
+    return reverse ? launch_kernel(after, scan_simt_kernel<DB, DV, true, true, In, Out>, grid, NT, 0, s, p)
+                   : launch_kernel(after, scan_simt_kernel<DB, DV, true, false, In, Out>, grid, NT, 0, s, p);
 }
 
 template <typename In, typename Out>
-cudaError_t launch_dims(const ScanArgs &p, int d_b, int d_v, bool reverse, bool states,
+cudaError_t launch_dims(const ScanArgs &p, int d_b, int d_v, bool reverse, bool states, bool after,
                         cudaStream_t s) {
     switch (d_b * 1000 + d_v) {
-        case 16016: return launch_shape<16, 16, In, Out>(p, reverse, states, s);
-        case 16032: return launch_shape<16, 32, In, Out>(p, reverse, states, s);
-        case 16064: return launch_shape<16, 64, In, Out>(p, reverse, states, s);
-        case 16128: return launch_shape<16, 128, In, Out>(p, reverse, states, s);
-        case 32016: return launch_shape<32, 16, In, Out>(p, reverse, states, s);
-        case 32032: return launch_shape<32, 32, In, Out>(p, reverse, states, s);
-        case 32064: return launch_shape<32, 64, In, Out>(p, reverse, states, s);
-        case 32128: return launch_shape<32, 128, In, Out>(p, reverse, states, s);
-        case 64016: return launch_shape<64, 16, In, Out>(p, reverse, states, s);
-        case 64032: return launch_shape<64, 32, In, Out>(p, reverse, states, s);
-        case 64064: return launch_shape<64, 64, In, Out>(p, reverse, states, s);
-        case 64128: return launch_shape<64, 128, In, Out>(p, reverse, states, s);
-        case 128016: return launch_shape<128, 16, In, Out>(p, reverse, states, s);
-        case 128032: return launch_shape<128, 32, In, Out>(p, reverse, states, s);
-        case 128064: return launch_shape<128, 64, In, Out>(p, reverse, states, s);
-        case 128128: return launch_shape<128, 128, In, Out>(p, reverse, states, s);
+        case 16016: return launch_shape<16, 16, In, Out>(p, reverse, states, after, s);
+        case 16032: return launch_shape<16, 32, In, Out>(p, reverse, states, after, s);
+        case 16064: return launch_shape<16, 64, In, Out>(p, reverse, states, after, s);
+        case 16128: return launch_shape<16, 128, In, Out>(p, reverse, states, after, s);
+        case 32016: return launch_shape<32, 16, In, Out>(p, reverse, states, after, s);
+        case 32032: return launch_shape<32, 32, In, Out>(p, reverse, states, after, s);
+        case 32064: return launch_shape<32, 64, In, Out>(p, reverse, states, after, s);
+        case 32128: return launch_shape<32, 128, In, Out>(p, reverse, states, after, s);
+        case 64016: return launch_shape<64, 16, In, Out>(p, reverse, states, after, s);
+        case 64032: return launch_shape<64, 32, In, Out>(p, reverse, states, after, s);
+        case 64064: return launch_shape<64, 64, In, Out>(p, reverse, states, after, s);
+        case 64128: return launch_shape<64, 128, In, Out>(p, reverse, states, after, s);
+        case 128016: return launch_shape<128, 16, In, Out>(p, reverse, states, after, s);
+        case 128032: return launch_shape<128, 32, In, Out>(p, reverse, states, after, s);
+        case 128064: return launch_shape<128, 64, In, Out>(p, reverse, states, after, s);
+        case 128128: return launch_shape<128, 128, In, Out>(p, reverse, states, after, s);
     }
     return cudaErrorInvalidValue;
 }
@@ -197,7 +196,12 @@ constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
 scan_join_kernel(const ScanArgs p, int elements, bool reverse) {
     __shared__ int scratch[34];
-    const int slot = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    const int h = blockIdx.x % p.H;
+    int slot = blockIdx.x / p.H;
+    launch_dependents();
+    wait_for_previous();
+    // equal lengths: a block for each sequence, else for each state, of which the first goes on
+    if (p.cu == nullptr) slot *= p.inner / p.N;
     const Segment seg = find_segment(p, slot, true, reverse, scratch, kJoinThreads);
     if (seg.n < 0 || seg.index != 0 || seg.count < 3) return;
     const int e = (blockIdx.y * kJoinThreads + threadIdx.x) * 4;
@@ -205,19 +209,19 @@ scan_join_kernel(const ScanArgs p, int elements, bool reverse) {
     const float w = expf(clamp_log_gate(p.decay[h]) * (float)p.seg_tokens);
     const size_t step = (size_t)p.H * elements / 4;
     float4 *at = reinterpret_cast<float4 *>(p.seg + ((size_t)seg.state * p.H + h) * elements + e);
-    float4 x = *at;
     const int end = min(seg.count - 1, p.inner - seg.state);
-    for (int s = 1; s < end; s += 4) {
-        float4 y[4];
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < end; s += 8) {   // eight loads in flight
+        float4 y[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 8; ++u)
             if (s + u < end) y[u] = at[(size_t)(s + u) * step];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 8; ++u) {
             if (s + u >= end) break;
             x = make_float4(fmaf(w, x.x, y[u].x), fmaf(w, x.y, y[u].y), fmaf(w, x.z, y[u].z),
                             fmaf(w, x.w, y[u].w));
-            at[(size_t)(s + u) * step] = x;
+            if (s + u > 0) at[(size_t)(s + u) * step] = x;
         }
     }
 }
@@ -229,6 +233,8 @@ constexpr int kSumThreads = 256;
 template <typename Out>
 __global__ void __launch_bounds__(kSumThreads)
 group_sum_kernel(const float *__restrict__ part, int64_t vecs, int group, int d4, Out *__restrict__ out) {
+    launch_dependents();
+    wait_for_previous();
     for (int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x; i < vecs;
          i += (int64_t)gridDim.x * kSumThreads) {
         const int64_t head = i / d4;
@@ -335,16 +341,15 @@ cudaError_t launch_step_dk(const void *q, const void *k, const void *v, const fl
 }  // namespace
 
 cudaError_t launch_scan_simt(const ScanArgs &p, int d_b, int d_v, bool reverse, bool states,
-                             bool bf16, bool out_f32, cudaStream_t stream) {
-    if (!bf16) return launch_dims<float, float>(p, d_b, d_v, reverse, states, stream);
-    if (out_f32) return launch_dims<__nv_bfloat16, float>(p, d_b, d_v, reverse, states, stream);
-    return launch_dims<__nv_bfloat16, __nv_bfloat16>(p, d_b, d_v, reverse, states, stream);
+                             bool bf16, bool out_f32, bool after, cudaStream_t stream) {
+    if (!bf16) return launch_dims<float, float>(p, d_b, d_v, reverse, states, after, stream);
+    if (out_f32) return launch_dims<__nv_bfloat16, float>(p, d_b, d_v, reverse, states, after, stream);
+    return launch_dims<__nv_bfloat16, __nv_bfloat16>(p, d_b, d_v, reverse, states, after, stream);
 }
 
 cudaError_t launch_scan_join(const ScanArgs &p, int elements, bool reverse, cudaStream_t stream) {
-    const dim3 grid((unsigned)p.inner * p.H, (elements / 4 + kJoinThreads - 1) / kJoinThreads);
-    scan_join_kernel<<<grid, kJoinThreads, 0, stream>>>(p, elements, reverse);
-    return cudaGetLastError();
+    const dim3 grid((unsigned)(p.cu == nullptr ? p.N : p.inner) * p.H, (elements / 4 + kJoinThreads - 1) / kJoinThreads);
+    return launch_kernel(true, scan_join_kernel, grid, kJoinThreads, 0, stream, p, elements, reverse);
 }
 
 cudaError_t launch_group_sum(const float *part, int64_t T, int H_qk, int group, int d, bool bf16,
@@ -352,12 +357,10 @@ cudaError_t launch_group_sum(const float *part, int64_t T, int H_qk, int group, 
     const int64_t vecs = T * H_qk * (d / 4);
     const unsigned grid = (unsigned)std::min<int64_t>((vecs + kSumThreads - 1) / kSumThreads, 148 * 16);
     if (bf16)
-        group_sum_kernel<<<grid, kSumThreads, 0, stream>>>(part, vecs, group, d / 4,
-                                                           static_cast<__nv_bfloat16 *>(out));
-    else
-        group_sum_kernel<<<grid, kSumThreads, 0, stream>>>(part, vecs, group, d / 4,
-                                                           static_cast<float *>(out));
-    return cudaGetLastError();
+        return launch_kernel(true, group_sum_kernel<__nv_bfloat16>, dim3(grid), kSumThreads, 0, stream, part, vecs,
+                             group, d / 4, static_cast<__nv_bfloat16 *>(out));
+    return launch_kernel(true, group_sum_kernel<float>, dim3(grid), kSumThreads, 0, stream, part, vecs, group, d / 4,
+                         static_cast<float *>(out));
 }
 
 cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, const float *decay,

@@ -202,60 +202,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         return;
     }
 
-    if (tid == 64) {
-        if (OUT) prefetch_tensormap(&ma);
-        prefetch_tensormap(&mb);
-        prefetch_tensormap(&mv);
-    }
-    if (tid == 0) {
-        for (int s = 0; s < 4; ++s) {
-            mbar_init(&m->full[s], 1);
-            mbar_init(&m->kv_full[s], 1);
-        }
-        for (int s = 0; s < 3; ++s) mbar_init(&m->done[s], 1);
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&m->w_full[b], kSThreads);
-            mbar_init(&m->w_full[2 + b], kSThreads);
-            mbar_init(&m->kv_free[b], kSThreads);
-            mbar_init(&m->sc_full[b], 1);
-            mbar_init(&m->p_full[b], kPThreads);
-            mbar_init(&m->o_free[b], kOThreads);
-        }
-        mbar_init(&m->s_full, kSThreads);
-        mbar_init(&m->end[0], 1);
-        mbar_init(&m->end[1], 1);
-        m->abort = 0;
-        fence_barrier_init();
-    }
-    const float g = clamp_log_gate(p.decay[h]);
-    if (tid <= C) m->pw[tid] = expf(g * (float)tid);
-    if (tid < C) m->lead[tid] = expf(g * (float)(REV ? C - 1 - tid : tid + 1));
-    if (warp == 0) {
-        tmem_alloc(&m->tmem, T_COLS);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = m->tmem;
     const uint32_t mbase = sbase + Sh::MISC;
 #define BAR(name, i) (mbase + (uint32_t)offsetof(Misc, name) + 8 * (i))
-    // Bounded wait of a whole warp; false, and everyone told, when it or another role
-    // gave up.  A phase that is complete already costs one look.
-    auto warp_wait = [&](uint32_t bar, uint32_t phase, uint32_t code) {
-        if (__all_sync(0xffffffffu, try_wait(bar, phase & 1))) return true;
-        if (wait_on(bar, phase & 1, BAR(abort, 0))) return true;
-        if (lane == 0) {
-            *reinterpret_cast<volatile int *>(&m->abort) = 1;
-            atomicOr(status, code);
-        }
-        return false;
-    };
-    const uint64_t kmajor = sw128_kmajor_desc(sbase), mnmajor = sw128_mnmajor_desc(sbase, 8192, 1024);
     // block b in scan order: its first token and its tokens
     auto block_t0 = [&](int b) { return seg.t0 + (REV ? blocks - 1 - b : b) * C; };
     auto block_n = [&](int b) { return min(C, seg.len - (REV ? blocks - 1 - b : b) * C); };
-
     auto load = [&](int b) {
         if (elect_one()) {
             const int ha = h / (p.H / p.HA), hb = h / (p.H / p.HB), hv = h / (p.H / p.HV);
@@ -275,12 +226,64 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             (void)mbar_wait_sleep(&m->full[b % Sh::NS], (b / Sh::NS) & 1);
     };
 
+    // the loader's first block is on its way before anything else is ready
+    int issued = 0;
+    if (warp == 3) {
+        if (elect_one()) {
+            for (int s = 0; s < 4; ++s) {
+                mbar_init(&m->full[s], 1);
+                mbar_init(&m->kv_full[s], 1);
+            }
+            for (int s = 0; s < 3; ++s) mbar_init(&m->done[s], 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&m->w_full[b], kSThreads);
+                mbar_init(&m->w_full[2 + b], kSThreads);
+                mbar_init(&m->kv_free[b], kSThreads);
+                mbar_init(&m->sc_full[b], 1);
+                mbar_init(&m->p_full[b], kPThreads);
+                mbar_init(&m->o_free[b], kOThreads);
+            }
+            mbar_init(&m->s_full, kSThreads);
+            mbar_init(&m->end[0], 1);
+            mbar_init(&m->end[1], 1);
+            m->abort = 0;
+            fence_barrier_init();
+            fence_proxy_async();
+        }
+        __syncwarp();
+        if (blocks > 0) load(issued++);
+    }
+    launch_dependents();
+    const float g = clamp_log_gate(p.decay[h]);
+    if (tid <= C) m->pw[tid] = expf(g * (float)tid);
+    if (tid < C) m->lead[tid] = expf(g * (float)(REV ? C - 1 - tid : tid + 1));
+    if (warp == 0) {
+        tmem_alloc(&m->tmem, T_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = m->tmem;
+    // Bounded wait of a whole warp; false, and everyone told, when it or another role
+    // gave up.  A phase that is complete already costs one look.
+    auto warp_wait = [&](uint32_t bar, uint32_t phase, uint32_t code) {
+        if (__all_sync(0xffffffffu, try_wait(bar, phase & 1))) return true;
+        if (wait_on(bar, phase & 1, BAR(abort, 0))) return true;
+        if (lane == 0) {
+            *reinterpret_cast<volatile int *>(&m->abort) = 1;
+            atomicOr(status, code);
+        }
+        return false;
+    };
+    const uint64_t kmajor = sw128_kmajor_desc(sbase), mnmajor = sw128_mnmajor_desc(sbase, 8192, 1024);
     if (warp >= 8) {
         // ------------------------------------------------ S: row r, 64 columns ----
         const int t = tid - kSThreads;
         const int r = (warp & 3) * 32 + lane, half = (warp - 8) >> 2;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         float2 S[32];
+        if (OUT) wait_for_previous();
         if (OUT && seg.index > 0) {   // states between segments lie in the order of these threads
             const float4 *src = reinterpret_cast<const float4 *>(
                 p.seg + ((size_t)(seg.state - 1) * p.H + h) * (D * D)) + t;
@@ -427,6 +430,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                     dst[i] = make_float4(S[2 * i].x, S[2 * i].y, S[2 * i + 1].x, S[2 * i + 1].y);
             }
         } else {
+            wait_for_previous();   // an earlier scan of this call may still read the states
             float4 *dst = reinterpret_cast<float4 *>(seg_out) + t;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -563,7 +567,6 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         (void)mbar_wait_sleep(&m->end[0], 0);
     } else if (warp == 3 && OUT) {
         // ------------------------------------------- issuer: S A^T and V^T P^T ----
-        int issued = 0;
         for (; issued < min(Sh::NS - 1, blocks); ++issued) load(issued);
         for (int b = 0; b < blocks; ++b) {
             // block b - 1 is done, and its state product, which the other issuer committed:
@@ -604,7 +607,6 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         drain(issued);
     } else if (warp == 3) {
         // ---------------------------------------- loader of the state's pass ----
-        int issued = 0;
         for (; issued < blocks; ++issued) {
             // a stage is free when the product that reads it is done
             const int f = issued - Sh::NS;
@@ -693,30 +695,30 @@ bool make_tile_map(CUtensorMap *map, const void *base, int total_T, int H) {
 
 template <bool OUT, bool REV, typename OutT>
 cudaError_t launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mv,
-                   const ScanArgs &p, cudaStream_t stream) {
+                   const ScanArgs &p, bool after, cudaStream_t stream) {
     auto fn = scan_tc_kernel<OUT, REV, OutT>;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(fn), smem_bytes<OUT>());
     if (e != cudaSuccess) return e;
-    fn<<<(unsigned)(OUT ? p.slots : p.inner) * p.H, kThreads, smem_bytes<OUT>(), stream>>>(ma, mb, mv, p);
-    return cudaGetLastError();
+    return launch_kernel(after, fn, dim3((unsigned)(OUT ? p.slots : p.inner) * p.H), kThreads, smem_bytes<OUT>(),
+                         stream, ma, mb, mv, p);
 }
 
 }  // namespace
 
-cudaError_t launch_scan_tc(const ScanArgs &p, bool reverse, bool states, bool out_f32,
+cudaError_t launch_scan_tc(const ScanArgs &p, bool reverse, bool states, bool out_f32, bool after,
                            cudaStream_t stream) {
     CUtensorMap ma, mb, mv;
     if (!make_tile_map(&ma, p.a, p.total_T, p.HA) || !make_tile_map(&mb, p.b, p.total_T, p.HB) ||
         !make_tile_map(&mv, p.v, p.total_T, p.HV))
         return cudaErrorInvalidValue;
     if (states)
-        return reverse ? launch<false, true, __nv_bfloat16>(ma, mb, mv, p, stream)
-                       : launch<false, false, __nv_bfloat16>(ma, mb, mv, p, stream);
+        return reverse ? launch<false, true, __nv_bfloat16>(ma, mb, mv, p, after, stream)
+                       : launch<false, false, __nv_bfloat16>(ma, mb, mv, p, after, stream);
     if (out_f32)
-        return reverse ? launch<true, true, float>(ma, mb, mv, p, stream)
-                       : launch<true, false, float>(ma, mb, mv, p, stream);
-    return reverse ? launch<true, true, __nv_bfloat16>(ma, mb, mv, p, stream)
-                   : launch<true, false, __nv_bfloat16>(ma, mb, mv, p, stream);
+        return reverse ? launch<true, true, float>(ma, mb, mv, p, after, stream)
+                       : launch<true, false, float>(ma, mb, mv, p, after, stream);
+    return reverse ? launch<true, true, __nv_bfloat16>(ma, mb, mv, p, after, stream)
+                   : launch<true, false, __nv_bfloat16>(ma, mb, mv, p, after, stream);
 }
 
 }  // namespace gdr
