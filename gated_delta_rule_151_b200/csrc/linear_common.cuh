@@ -29,7 +29,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "common.cuh"
+#include "launch.cuh"
 
 namespace gdr {
 
@@ -131,30 +131,6 @@ __device__ inline Segment find_segment(const ScanArgs &p, int slot, bool inner, 
     s.t0 = t0 + place * p.seg_tokens;
     s.len = min(p.seg_tokens, len - place * p.seg_tokens);
     return s;
-}
-
-// The kernels of one call follow each other without draining the GPU between them:
-// each lets the next one start once its own blocks have, and waits for the one
-// before to be complete where it first touches memory that passes between them.
-// Every kernel launched with `after` waits in every block that has work, so a
-// kernel is complete only when all before it in the call are.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-template <typename... Params, typename... Args>
-cudaError_t launch_kernel(bool after, void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
-                          cudaStream_t stream, Args... args) {
-    cudaLaunchConfig_t c = {};
-    c.gridDim = grid;
-    c.blockDim = dim3(threads);
-    c.dynamicSmemBytes = smem;
-    c.stream = stream;
-    cudaLaunchAttribute a = {};
-    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    a.val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = &a;
-    c.numAttrs = after ? 1 : 0;
-    return cudaLaunchKernelEx(&c, kernel, Params(args)...);
 }
 
 // Launchers.  `states`: the pass that writes the segments' own states (all but

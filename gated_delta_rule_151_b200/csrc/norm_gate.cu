@@ -5,9 +5,9 @@
 //     n = y / sqrt(mean y^2 + eps) * w2
 //
 // Every tensor is read and written once, 16 bytes a load, and HBM bounds both.
-// A row belongs to TPR threads, eight neighbouring channels (a vector) per
-// thread and step of TPR vectors; it stays in registers between its norms, so
-// the second norm costs no second read.  Sums are fp32: over a thread's
+// A row belongs to TPR threads, 16-byte pieces of it to a thread; it stays in
+// registers between its norms, so the second norm costs no second read, while the
+// next row is on its way to shared memory.  Sums are fp32: over a thread's
 // channels, then over the row's threads by a butterfly (and, beyond a warp, in
 // the order of the warps).  n is taken from y before y is rounded.
 //
@@ -26,33 +26,31 @@
 #include "norm_gate.h"
 
 #include <algorithm>
+#include <atomic>
 
-#include "common.cuh"
+#include "launch.cuh"
 
 namespace gdr {
 namespace {
 
 constexpr int kSMs = 148;
 
-__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&f)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// A piece is 16 bytes of a row: E channels, 8 in bf16 and 4 in fp32.
+template <int E>
+__device__ __forceinline__ void load_weights(const float *p, float (&f)[E]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int e = 0; e < E; e += 4) {
+        const float4 a = *reinterpret_cast<const float4 *>(p + e);
+        f[e] = a.x; f[e + 1] = a.y; f[e + 2] = a.z; f[e + 3] = a.w;
     }
 }
-__device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+template <int E>
+__device__ __forceinline__ void store_floats(float *p, const float (&f)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; e += 4) *reinterpret_cast<float4 *>(p + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8]) {
+__device__ __forceinline__ void store_piece(float *p, const float (&f)[4]) { store_floats(p, f); }
+__device__ __forceinline__ void store_piece(__nv_bfloat16 *p, const float (&f)[8]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -62,7 +60,9 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8]) {
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+// Single-instruction exponential and reciprocal: together within 2^-21 (1 + |z| / 8) of
+// the value.  The full-precision pair took the heads' forward pass from 23 to 35 us.
+__device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.0f + ex2_approx(-kLog2e * z)); }
 
 // act(z) and, for the gradient, act'(z).
 __device__ __forceinline__ float act_of(int act, float z) {
@@ -109,123 +109,215 @@ __device__ __forceinline__ void row_sum(float (&x)[NV], float *scratch, int &tur
     }
 }
 
+constexpr int kStages = 2;   // row groups a block holds: one at work, one on its way (three gained nothing)
+constexpr int kMostRing = 200 * 1024;
+
 template <typename T, int TPR, int VPT>
 struct Shape {
     static constexpr int NT = TPR > 256 ? TPR : 256;
-    static constexpr int ROWS = NT / TPR;      // rows of a block at a time
+    static constexpr int ROWS = NT / TPR;                  // rows of a block at a time
+    static constexpr int E = 16 / sizeof(T);
 };
 
-template <typename T, int TPR, int VPT>
+// A thread's pieces of the next row groups, copied to shared memory without
+// registers while it works on this one.  Each thread reads only what it copied
+// itself: no barriers.  `Tensors` rows side by side.  Rows too wide for it (fp32
+// gradients beyond 4096 channels, every row beyond 8192) are read from memory where they
+// are used.
+template <typename T, int TPR, int VPT, int Tensors>
+struct Ring {
+    using Sh = Shape<T, TPR, VPT>;
+    static constexpr int WANTED = kStages * Tensors * VPT * Sh::NT * 16;
+    static constexpr bool STAGED = WANTED <= kMostRing;
+    static constexpr int BYTES = STAGED ? WANTED : 0;
+    uint32_t base;
+
+    __device__ __forceinline__ uint32_t place(int stage, int tensor, int i) const {
+        return base + (((stage * Tensors + tensor) * VPT + i) * Sh::NT) * 16;
+    }
+    __device__ __forceinline__ void copy(int stage, int tensor, int i, const T *src) const {
+        if (STAGED)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(place(stage, tensor, i)), "l"(src) : "memory");
+    }
+    __device__ __forceinline__ void read(int stage, int tensor, int i, const T *src, float (&f)[Sh::E]) const {
+        uint32_t w[4];
+        if (STAGED) {
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(place(stage, tensor, i))
+                         : "memory");
+        } else {
+            const uint4 x = *reinterpret_cast<const uint4 *>(src);
+            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        }
+#pragma unroll
+        for (int e = 0; e < Sh::E; ++e) {
+            if (sizeof(T) == 4) f[e] = __uint_as_float(w[e & 3]);
+            else f[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+        }
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory"); }
+};
+
+// GATE: a gate is given; NEXT: next_weight is.
+template <typename T, int TPR, int VPT, bool GATE, bool NEXT>
 __global__ void __launch_bounds__(Shape<T, TPR, VPT>::NT)
 norm_gate_kernel(const NormArgs p) {
     using Sh = Shape<T, TPR, VPT>;
+    constexpr int E = Sh::E;
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float scratch[64];
-    int turn = 0;
-    const int lane = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * Sh::ROWS + threadIdx.x / TPR;
-    const int vecs = p.dim / 8;
-    const bool live = row < p.rows;
-    const int64_t at = row * p.dim;
-    const T *x_ = static_cast<const T *>(p.x), *z_ = static_cast<const T *>(p.gate);
-    const T *res_ = static_cast<const T *>(p.residual);
-
-    float y[VPT][8], z[VPT][8], res[VPT][8];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = lane + i * TPR;
-        const bool in = live && c < vecs;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) { y[i][e] = 0.f; z[i][e] = 1.f; res[i][e] = 0.f; }
-        if (in) {
-            load8(x_ + at + c * 8, y[i]);
-            if (z_ != nullptr) load8(z_ + at + c * 8, z[i]);
-            if (res_ != nullptr) load8(res_ + at + c * 8, res[i]);
-        }
-    }
-    float r = 1.f;
-    if (p.weight != nullptr) {
-        float s[1] = {0.f};
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[0] = fmaf(y[i][e], y[i][e], s[0]);
-        row_sum<TPR>(s, scratch, turn);
-        r = rsqrtf(s[0] * p.inv_dim + p.eps);
-    }
-    float s2[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = lane + i * TPR;
-        const bool in = live && c < vecs;
-        float w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 1.f;
-        if (in && p.weight != nullptr) load8(p.weight + c * 8, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float u = y[i][e] * r * w[e];
-            if (z_ != nullptr) u *= act_of(p.act, z[i][e]);
-            y[i][e] = res_ != nullptr ? fmaf(p.scale, u, res[i][e]) : p.scale * u;
-            s2[0] = fmaf(y[i][e], y[i][e], s2[0]);
-        }
-        if (in) store8(static_cast<T *>(p.y) + at + c * 8, y[i]);
-    }
-    if (p.next_weight == nullptr) return;
-    row_sum<TPR>(s2, scratch, turn);
-    const float r2 = rsqrtf(s2[0] * p.inv_dim + p.eps);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = lane + i * TPR;
-        if (live && c < vecs) {
-            float w[8];
-            load8(p.next_weight + c * 8, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] *= y[i][e] * r2;
-            store8(static_cast<T *>(p.y_norm) + at + c * 8, w);
-        }
-    }
-}
-
-template <typename T, int TPR, int VPT>
-__global__ void __launch_bounds__(Shape<T, TPR, VPT>::NT)
-norm_gate_backward_kernel(const NormArgs p) {
-    using Sh = Shape<T, TPR, VPT>;
-    __shared__ float scratch[64];
-    __shared__ float sums[Sh::ROWS > 1 ? Sh::NT * 8 : 1];
+    const Ring<T, TPR, VPT, 2 + GATE> ring{static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * 16};
     int turn = 0;
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
-    const int vecs = p.dim / 8;
+    const int pieces = p.dim / E;
     const T *x_ = static_cast<const T *>(p.x), *z_ = static_cast<const T *>(p.gate);
     const T *res_ = static_cast<const T *>(p.residual);
-    const T *dy_ = static_cast<const T *>(p.dy), *dn_ = static_cast<const T *>(p.dn);
+    const int64_t stride = (int64_t)gridDim.x * Sh::ROWS, first = (int64_t)blockIdx.x * Sh::ROWS + group;
 
-    float dw[VPT][8], dw2[VPT][8];
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < p.rows) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+            for (int i = 0; i < VPT; ++i) {
+                const int c = lane + i * TPR;
+                if (c >= pieces) continue;
+                const int64_t at = row * p.dim + c * E;
+                ring.copy(stage, 0, i, x_ + at);
+                if (res_ != nullptr) ring.copy(stage, 1, i, res_ + at);
+                if (GATE) ring.copy(stage, 1 + GATE, i, z_ + at);
+            }
+        }
+        ring.commit();
+    };
+    float w[VPT][E], w2[VPT][E];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[i][e] = dw2[i][e] = 0.f;
-
-    for (int64_t r0 = (int64_t)blockIdx.x * Sh::ROWS; r0 < p.rows; r0 += (int64_t)gridDim.x * Sh::ROWS) {
-        const int64_t row = r0 + group;
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + i * TPR;
+#pragma unroll
+        for (int e = 0; e < E; ++e) { w[i][e] = 1.f; w2[i][e] = 0.f; }
+        if (c < pieces && p.weight != nullptr) load_weights(p.weight + c * E, w[i]);
+        if (c < pieces && NEXT) load_weights(p.next_weight + c * E, w2[i]);
+    }
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) fetch(first + s * stride, s);
+    int stage = 0;
+    for (int64_t row = first; row - group < p.rows; row += stride) {
+        fetch(row + (kStages - 1) * stride, stage == 0 ? kStages - 1 : stage - 1);
+        ring.wait();
         const bool live = row < p.rows;
-        const int64_t at = row * p.dim;
-        float x[VPT][8], z[VPT][8], g[VPT][8], y[VPT][8], t[VPT][8];
+        float y[VPT][E];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[i][e] = 0.f;
+            if (live && lane + i * TPR < pieces) ring.read(stage, 0, i, x_ + row * p.dim + (lane + i * TPR) * E, y[i]);
+        }
+        float r = 1.f;
+        if (p.weight != nullptr) {
+            float s[1] = {0.f};
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                for (int e = 0; e < E; ++e) s[0] = fmaf(y[i][e], y[i][e], s[0]);
+            row_sum<TPR>(s, scratch, turn);
+            r = rsqrtf(s[0] * p.inv_dim + p.eps);
+        }
+        float s2[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = lane + i * TPR;
-            const bool in = live && c < vecs;
+            if (live && c < pieces) {
+                float z[E], res[E];
+                const int64_t at = row * p.dim + c * E;
+                if (GATE) ring.read(stage, 1 + GATE, i, z_ + at, z);
+                if (res_ != nullptr) ring.read(stage, 1, i, res_ + at, res);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[i][e] = 0.f; z[i][e] = 0.f; g[i][e] = 0.f; y[i][e] = 0.f; t[i][e] = 0.f;
-            }
-            if (in) {
-                load8(x_ + at + c * 8, x[i]);
-                if (z_ != nullptr) load8(z_ + at + c * 8, z[i]);
-                if (dy_ != nullptr) load8(dy_ + at + c * 8, g[i]);
-                if (dn_ != nullptr) {
-                    load8(dn_ + at + c * 8, t[i]);
-                    if (res_ != nullptr) load8(res_ + at + c * 8, y[i]);
+                for (int e = 0; e < E; ++e) {
+                    float u = y[i][e] * r * w[i][e];
+                    if (GATE) u *= act_of(p.act, z[e]);
+                    y[i][e] = res_ != nullptr ? fmaf(p.scale, u, res[e]) : p.scale * u;
+                    if (NEXT) s2[0] = fmaf(y[i][e], y[i][e], s2[0]);
                 }
+                store_piece(static_cast<T *>(p.y) + row * p.dim + c * E, y[i]);
+            }
+        }
+        if (NEXT) {
+            row_sum<TPR>(s2, scratch, turn);
+            const float r2 = rsqrtf(s2[0] * p.inv_dim + p.eps);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = lane + i * TPR;
+                if (live && c < pieces) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) y[i][e] *= r2 * w2[i][e];
+                    store_piece(static_cast<T *>(p.y_norm) + row * p.dim + c * E, y[i]);
+                }
+            }
+        }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+}
+
+// GATE: a gate is given; NEXT: dn is (and next_weight).
+template <typename T, int TPR, int VPT, bool GATE, bool NEXT>
+__global__ void __launch_bounds__(Shape<T, TPR, VPT>::NT, TPR > 256 || VPT > 2 ? 1 : 2)
+norm_gate_backward_kernel(const NormArgs p) {
+    using Sh = Shape<T, TPR, VPT>;
+    constexpr int E = Sh::E;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float scratch[64];
+    const Ring<T, TPR, VPT, 2 + GATE + 2 * NEXT> ring{static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * 16};
+    int turn = 0;
+    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    const int pieces = p.dim / E;
+    const T *x_ = static_cast<const T *>(p.x), *z_ = static_cast<const T *>(p.gate);
+    const T *res_ = static_cast<const T *>(p.residual);
+    const T *dy_ = static_cast<const T *>(p.dy), *dn_ = static_cast<const T *>(p.dn);
+    const int64_t stride = (int64_t)gridDim.x * Sh::ROWS, first = (int64_t)blockIdx.x * Sh::ROWS + group;
+
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < p.rows) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = lane + i * TPR;
+                if (c >= pieces) continue;
+                const int64_t at = row * p.dim + c * E;
+                ring.copy(stage, 0, i, x_ + at);
+                if (dy_ != nullptr) ring.copy(stage, 1, i, dy_ + at);
+                if (GATE) ring.copy(stage, 2, i, z_ + at);
+                if (NEXT) ring.copy(stage, 2 + GATE, i, dn_ + at);
+                if (NEXT && res_ != nullptr) ring.copy(stage, 3 + GATE, i, res_ + at);
+            }
+        }
+        ring.commit();
+    };
+    float dw[VPT][E], dw2[VPT][E], w[VPT][E], w2[VPT][E];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + i * TPR;
+#pragma unroll
+        for (int e = 0; e < E; ++e) { dw[i][e] = dw2[i][e] = 0.f; w[i][e] = 1.f; w2[i][e] = 0.f; }
+        if (c < pieces && p.weight != nullptr) load_weights(p.weight + c * E, w[i]);
+        if (c < pieces && NEXT) load_weights(p.next_weight + c * E, w2[i]);
+    }
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) fetch(first + s * stride, s);
+    int stage = 0;
+    for (int64_t row = first; row - group < p.rows; row += stride) {
+        fetch(row + (kStages - 1) * stride, stage == 0 ? kStages - 1 : stage - 1);
+        ring.wait();
+        const bool live = row < p.rows;
+        const int64_t at = row * p.dim;
+        float x[VPT][E], g[VPT][E];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) { x[i][e] = 0.f; g[i][e] = 0.f; }
+            if (live && lane + i * TPR < pieces) {
+                const int64_t here = at + (lane + i * TPR) * E;
+                ring.read(stage, 0, i, x_ + here, x[i]);
+                if (dy_ != nullptr) ring.read(stage, 1, i, dy_ + here, g[i]);
             }
         }
         float r = 1.f;
@@ -234,193 +326,212 @@ norm_gate_backward_kernel(const NormArgs p) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s[0] = fmaf(x[i][e], x[i][e], s[0]);
+                for (int e = 0; e < E; ++e) s[0] = fmaf(x[i][e], x[i][e], s[0]);
             row_sum<TPR>(s, scratch, turn);
             r = rsqrtf(s[0] * p.inv_dim + p.eps);
         }
-        if (dn_ != nullptr) {
+        float a[VPT][E], da[VPT][E];           // act(z) and act'(z)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float z[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) z[e] = 0.f;
+            if (GATE && live && lane + i * TPR < pieces) ring.read(stage, 2, i, z_ + at + (lane + i * TPR) * E, z);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                a[i][e] = 1.f;
+                da[i][e] = 0.f;
+                if (GATE) act_both(p.act, z[e], a[i][e], da[i][e]);
+                x[i][e] *= r;                  // xh
+            }
+        }
+        if (NEXT) {
             // y again, and the two sums of the second norm
-            float s[2] = {0.f, 0.f};
+            float s[2] = {0.f, 0.f}, y[VPT][E], t[VPT][E];
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int c = lane + i * TPR;
-                const bool in = live && c < vecs;
-                float w[8], w2[8];
+                const bool in = live && lane + i * TPR < pieces;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = w2[e] = 1.f;
-                if (in && p.weight != nullptr) load8(p.weight + c * 8, w);
-                if (in) load8(p.next_weight + c * 8, w2);
+                for (int e = 0; e < E; ++e) { y[i][e] = 0.f; t[i][e] = 0.f; }
+                const int64_t here = at + (lane + i * TPR) * E;
+                if (in) ring.read(stage, 2 + GATE, i, dn_ + here, t[i]);
+                if (in && res_ != nullptr) ring.read(stage, 3 + GATE, i, res_ + here, y[i]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float u = x[i][e] * r * w[e];
-                    if (z_ != nullptr) u *= act_of(p.act, z[i][e]);
+                for (int e = 0; e < E; ++e) {
+                    float u = x[i][e] * w[i][e];
+                    if (GATE) u *= a[i][e];
                     y[i][e] = fmaf(p.scale, u, y[i][e]);
                     s[0] = fmaf(y[i][e], y[i][e], s[0]);
-                    s[1] = fmaf(t[i][e] * w2[e], y[i][e], s[1]);
+                    s[1] = fmaf(t[i][e] * w2[i][e], y[i][e], s[1]);
                 }
             }
             row_sum<TPR>(s, scratch, turn);
             const float r2 = rsqrtf(s[0] * p.inv_dim + p.eps);
             const float m = s[1] * r2 * p.inv_dim;       // mean(dn w2 yh)
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int c = lane + i * TPR;
-                float w2[8];
+            for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w2[e] = 0.f;
-                if (live && c < vecs) load8(p.next_weight + c * 8, w2);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < E; ++e) {
                     const float yh = y[i][e] * r2;
                     dw2[i][e] = fmaf(t[i][e], yh, dw2[i][e]);
-                    g[i][e] = fmaf(r2, fmaf(-yh, m, t[i][e] * w2[e]), g[i][e]);
+                    g[i][e] = fmaf(r2, fmaf(-yh, m, t[i][e] * w2[i][e]), g[i][e]);
                 }
-            }
         }
         float s[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = lane + i * TPR;
-            const bool in = live && c < vecs;
-            if (in && p.dresidual != nullptr) store8(static_cast<T *>(p.dresidual) + at + c * 8, g[i]);
-            float w[8], dz[8];
+            const bool in = live && c < pieces;
+            if (in && p.dresidual != nullptr) store_piece(static_cast<T *>(p.dresidual) + at + c * E, g[i]);
+            float dz[E];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = 1.f;
-            if (in && p.weight != nullptr) load8(p.weight + c * 8, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float du = p.scale * g[i][e], xh = x[i][e] * r;
-                float a = 1.f, da = 0.f;
-                if (z_ != nullptr) act_both(p.act, z[i][e], a, da);
-                dz[e] = du * xh * w[e] * da;
-                const float dua = du * a;
-                dw[i][e] = fmaf(dua, xh, dw[i][e]);
-                g[i][e] = dua * w[e];
-                s[0] = fmaf(g[i][e], xh, s[0]);
-                x[i][e] = xh;
+            for (int e = 0; e < E; ++e) {
+                const float du = p.scale * g[i][e], dua = du * a[i][e];
+                dz[e] = du * x[i][e] * w[i][e] * da[i][e];
+                dw[i][e] = fmaf(dua, x[i][e], dw[i][e]);
+                g[i][e] = dua * w[i][e];
+                s[0] = fmaf(g[i][e], x[i][e], s[0]);
             }
-            if (in && z_ != nullptr) store8(static_cast<T *>(p.dgate) + at + c * 8, dz);
+            if (GATE && in) store_piece(static_cast<T *>(p.dgate) + at + c * E, dz);
         }
         if (p.weight != nullptr) row_sum<TPR>(s, scratch, turn);
         const float m = p.weight != nullptr ? s[0] * p.inv_dim : 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = lane + i * TPR;
-            if (live && c < vecs) {
+            if (live && c < pieces) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[i][e] = r * fmaf(-x[i][e], m, g[i][e]);
-                store8(static_cast<T *>(p.dx) + at + c * 8, x[i]);
+                for (int e = 0; e < E; ++e) x[i][e] = r * fmaf(-x[i][e], m, g[i][e]);
+                store_piece(static_cast<T *>(p.dx) + at + c * E, x[i]);
             }
         }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
+    __shared__ float sums[Sh::ROWS > 1 ? Sh::NT * E : 1];
 
+    launch_dependents();
     // the block's sums: over its row groups in their order, then one partial row
-    auto put = [&](float (&v)[VPT][8], float *part) {
+    auto put = [&](float (&v)[VPT][E], float *part) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = lane + i * TPR;
             if constexpr (Sh::ROWS > 1) {
                 __syncthreads();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sums[e * Sh::NT + threadIdx.x] = v[i][e];
+                for (int e = 0; e < E; ++e) sums[e * Sh::NT + threadIdx.x] = v[i][e];
                 __syncthreads();
                 if (group == 0) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (int e = 0; e < E; ++e)
                         for (int q = 1; q < Sh::ROWS; ++q) v[i][e] += sums[e * Sh::NT + q * TPR + lane];
                 }
             }
-            if (group == 0 && c < vecs) store8(part + (int64_t)blockIdx.x * p.dim + c * 8, v[i]);
+            if (group == 0 && c < pieces) store_floats(part + (int64_t)blockIdx.x * p.dim + c * E, v[i]);
         }
     };
     if (p.weight != nullptr) put(dw, p.part);
-    if (dn_ != nullptr) put(dw2, p.part2);
+    if (NEXT) put(dw2, p.part2);
 }
 
-// Partial rows -> the weights' gradients: 32 columns a block, eight runs of
-// partial rows added up side by side, then the runs in their order.
+// Partial rows -> the weights' gradients: 8 columns a block, 32 runs of partial rows
+// added up side by side, then the runs in their order.
 __global__ void __launch_bounds__(256)
 norm_sums_kernel(const float *part, float *dw, const float *part2, float *dw2, int blocks, int dim) {
-    __shared__ float s[8][33];
+    __shared__ float s[32][9];
     const float *src = blockIdx.y == 0 ? part : part2;
     float *dst = blockIdx.y == 0 ? dw : dw2;
+    wait_for_previous();
     if (dst == nullptr) return;
-    const int col = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
+    const int x = threadIdx.x & 7, run = threadIdx.x >> 3, col = blockIdx.x * 8 + x;
+    const int per = (blocks + 31) / 32, end = min(blocks, (run + 1) * per);
     float sum = 0.f;
-    if (col < dim) {
-        const int per = (blocks + 7) / 8;
-        const int b1 = min(blocks, (run + 1) * per);
 #pragma unroll 8
-        for (int b = run * per; b < b1; ++b) sum += src[(int64_t)b * dim + col];
-    }
-    s[run][threadIdx.x & 31] = sum;
+    for (int b = run * per; b < end; ++b) sum += src[(int64_t)b * dim + col];
+    s[run][x] = sum;
     __syncthreads();
-    if (run == 0 && col < dim) {
+    if (run == 0) {
 #pragma unroll
-        for (int q = 1; q < 8; ++q) sum += s[q][threadIdx.x];
+        for (int q = 1; q < 32; ++q) sum += s[q][x];
         dst[col] = sum;
     }
 }
 
-template <typename T, int TPR, int VPT>
-cudaError_t launch_forward(const NormArgs &p, cudaStream_t s) {
-    using Sh = Shape<T, TPR, VPT>;
-    const int64_t blocks = (p.rows + Sh::ROWS - 1) / Sh::ROWS;
-    norm_gate_kernel<T, TPR, VPT><<<(unsigned)blocks, Sh::NT, 0, s>>>(p);
-    return cudaGetLastError();
-}
-
-template <typename T, int TPR, int VPT>
-cudaError_t launch_backward_rows(const NormArgs &p, cudaStream_t s) {
-    using Sh = Shape<T, TPR, VPT>;
-    const unsigned blocks = (unsigned)norm_gate_blocks(p.rows, p.dim);
-    norm_gate_backward_kernel<T, TPR, VPT><<<blocks, Sh::NT, 0, s>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || (p.dweight == nullptr && p.dnext_weight == nullptr)) return e;
-    norm_sums_kernel<<<dim3((p.dim + 31) / 32, p.dnext_weight != nullptr ? 2 : 1), 256, 0, s>>>(
-        p.part, p.dweight, p.part2, p.dnext_weight, (int)blocks, p.dim);
-    return cudaGetLastError();
-}
-
 // Threads of a row: the power of two that gives each one vector, as far as 512
-// threads reach; then several vectors a thread.
+// threads reach; then several vectors a thread (two and four a thread at smaller
+// widths took the heads' passes from 23 and 58 us to 28 and 83: what hides the
+// memory's latency is threads).
 int threads_of(int dim) {
     int t = 1;
     while (t < 512 && t * 8 < dim) t *= 2;
     return t;
 }
 
-template <typename T, bool BACK, int TPR, int VPT>
+// Blocks of the grid-stride loops: those that the GPU holds at once (a part of a
+// second round would leave most of it idle), and at most this many an SM, which
+// bounds the gradient's partial rows.
+int most_per_sm(int dim) { return threads_of(dim) > 256 ? 2 : 4; }
+
+template <typename Kernel>
+int64_t blocks_of(Kernel kernel, std::atomic<int> &resident, int threads, int rows_at_once, int bytes, const NormArgs &p) {
+    int per_sm = resident.load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, bytes) != cudaSuccess || per_sm < 1)
+            per_sm = 1;
+        resident.store(per_sm, std::memory_order_relaxed);
+    }
+    const int64_t groups = (p.rows + rows_at_once - 1) / rows_at_once;
+    return std::min<int64_t>(groups, (int64_t)std::min(per_sm, most_per_sm(p.dim)) * kSMs);
+}
+
+template <typename T, bool BACK, int TPR, int VPT, bool GATE, bool NEXT>
 cudaError_t launch_as(const NormArgs &p, cudaStream_t s) {
-    if constexpr (BACK) return launch_backward_rows<T, TPR, VPT>(p, s);
-    else return launch_forward<T, TPR, VPT>(p, s);
+    using Sh = Shape<T, TPR, VPT>;
+    auto kernel = BACK ? norm_gate_backward_kernel<T, TPR, VPT, GATE, NEXT> : norm_gate_kernel<T, TPR, VPT, GATE, NEXT>;
+    constexpr int bytes = BACK ? Ring<T, TPR, VPT, 2 + GATE + 2 * NEXT>::BYTES : Ring<T, TPR, VPT, 2 + GATE>::BYTES;
+    static std::atomic<int> resident{0};
+    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = blocks_of(kernel, resident, Sh::NT, Sh::ROWS, bytes, p);
+    kernel<<<(unsigned)blocks, Sh::NT, bytes, s>>>(p);
+    e = cudaGetLastError();
+    if (!BACK || e != cudaSuccess || (p.dweight == nullptr && p.dnext_weight == nullptr)) return e;
+    return launch_kernel(true, norm_sums_kernel, dim3(p.dim / 8, p.dnext_weight != nullptr ? 2 : 1), 256, 0, s, p.part,
+                         p.dweight, p.part2, p.dnext_weight, (int)blocks, p.dim);
+}
+
+template <typename T, bool BACK, int TPR, int VPT>
+cudaError_t launch_flags(const NormArgs &p, cudaStream_t s) {
+    const bool gate = p.gate != nullptr, next = BACK ? p.dn != nullptr : p.next_weight != nullptr;
+    if (gate) return next ? launch_as<T, BACK, TPR, VPT, true, true>(p, s) : launch_as<T, BACK, TPR, VPT, true, false>(p, s);
+    return next ? launch_as<T, BACK, TPR, VPT, false, true>(p, s) : launch_as<T, BACK, TPR, VPT, false, false>(p, s);
 }
 
 template <typename T, bool BACK>
 cudaError_t launch_any(const NormArgs &p, cudaStream_t s) {
+    constexpr int V = sizeof(T) / 2;     // pieces of a vector
     switch (threads_of(p.dim)) {
-        case 1: return launch_as<T, BACK, 1, 1>(p, s);
-        case 2: return launch_as<T, BACK, 2, 1>(p, s);
-        case 4: return launch_as<T, BACK, 4, 1>(p, s);
-        case 8: return launch_as<T, BACK, 8, 1>(p, s);
-        case 16: return launch_as<T, BACK, 16, 1>(p, s);
-        case 32: return launch_as<T, BACK, 32, 1>(p, s);
-        case 64: return launch_as<T, BACK, 64, 1>(p, s);
-        case 128: return launch_as<T, BACK, 128, 1>(p, s);
-        case 256: return launch_as<T, BACK, 256, 1>(p, s);
+        case 1: return launch_flags<T, BACK, 1, V>(p, s);
+        case 2: return launch_flags<T, BACK, 2, V>(p, s);
+        case 4: return launch_flags<T, BACK, 4, V>(p, s);
+        case 8: return launch_flags<T, BACK, 8, V>(p, s);
+        case 16: return launch_flags<T, BACK, 16, V>(p, s);
+        case 32: return launch_flags<T, BACK, 32, V>(p, s);
+        case 64: return launch_flags<T, BACK, 64, V>(p, s);
+        case 128: return launch_flags<T, BACK, 128, V>(p, s);
+        case 256: return launch_flags<T, BACK, 256, V>(p, s);
     }
-    if (p.dim <= 4096) return launch_as<T, BACK, 512, 1>(p, s);
-    if (p.dim <= 8192) return launch_as<T, BACK, 512, 2>(p, s);
-    return launch_as<T, BACK, 512, 4>(p, s);
+    if (p.dim <= 4096) return launch_flags<T, BACK, 512, V>(p, s);
+    if (p.dim <= 8192) return launch_flags<T, BACK, 512, 2 * V>(p, s);
+    return launch_flags<T, BACK, 512, 4 * V>(p, s);
 }
 
 }  // namespace
 
-// Blocks of the gradient's grid-stride loop: as many as the GPU holds at once.
+// At most this many blocks of the gradient's pass, each with a partial row of either
+// weight's gradient.
 int norm_gate_blocks(int64_t rows, int dim) {
     const int t = threads_of(dim), per = t > 256 ? 1 : 256 / t;
-    const int64_t all = (rows + per - 1) / per;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(all, t > 256 ? kSMs * 2 : kSMs * 4));
+    return (int)std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, most_per_sm(dim) * kSMs));
 }
 
 cudaError_t launch_norm_gate(const NormArgs &p, bool bf16, cudaStream_t stream) {
