@@ -9,6 +9,7 @@ fallback: if libgdr.so is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -62,6 +63,8 @@ _lib = None
 def load_library():
     """Load libgdr.so once (raises if it is missing: there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -560,50 +563,38 @@ def gdr_backward(q, k, v, g, beta, initial_state=None, cu_seqlens=None, *, d_o,
 _ACTIVATIONS = {"none": GDR_ACT_NONE, "silu": GDR_ACT_SILU, "sigmoid": GDR_ACT_SIGMOID}
 
 
-class _On:
-    """Makes ``device`` and ``stream`` current for a call; ``ptr`` is the stream's handle."""
-
-    def __init__(self, device, stream):
-        self._where, self._device = device, None
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self._device = torch.cuda.device(device)
-        self._given, self._stream = stream, None
-
-    def __enter__(self):
-        given = self._given
-        if given is not None and not isinstance(given, int) and given.device != self._where:
-            raise ValueError(f"stream is on {given.device}, the tensors on {self._where}")
-        if self._device is not None:
-            self._device.__enter__()
-        if given is None:
-            given = torch.cuda.current_stream()
-        else:
-            if isinstance(given, int):
-                given = torch.cuda.ExternalStream(given)
-            self._stream = torch.cuda.stream(given)
-            self._stream.__enter__()
-        self.ptr = ctypes.c_void_p(given.cuda_stream)
-        return self
-
-    def __exit__(self, *exc):
-        if self._stream is not None:
-            self._stream.__exit__(*exc)
-        if self._device is not None:
-            self._device.__exit__(*exc)
+def _on(device, stream, run):
+    """run(handle of the stream), with ``device`` and ``stream`` current."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return run(torch.cuda.current_stream().cuda_stream)
+    if stream is not None and not isinstance(stream, int) and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.device(device):
+        if stream is None:
+            return run(torch.cuda.current_stream().cuda_stream)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(stream):
+            return run(stream.cuda_stream)
 
 
 def _given(t, name, shape, dtype, device):
     """One tensor argument: on the device, contiguous, of this type and shape."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t is None:
         raise ValueError(f"{name} is required")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _scratch(workspace, need, device):
@@ -623,29 +614,33 @@ def _linear_args(q, k, v, decay, cu_seqlens, num_seqs):
     _need(v, "v", q.dtype, 3)
     T, Hqk, dk = q.shape
     H, dv = v.shape[1], v.shape[2]
-    dev = q.device
-    _given(k, "k", (T, Hqk, dk), q.dtype, dev)
-    _given(v, "v", (T, H, dv), q.dtype, dev)
+    dev, io = q.device, q.dtype
+    _given(k, "k", q.shape, io, dev)
+    _given(v, "v", (T, H, dv), io, dev)
     _given(decay, "decay", (H,), torch.float32, dev)
     if cu_seqlens is not None:
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-            raise ValueError("cu_seqlens must be [N + 1]")
         N = cu_seqlens.numel() - 1
+        if N < 0:
+            raise ValueError("cu_seqlens must be [N + 1]")
         _given(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
         if num_seqs is not None and int(num_seqs) != N:
             raise ValueError(f"num_seqs is {num_seqs}, cu_seqlens has {N} sequences")
     else:
         N = 1 if num_seqs is None else int(num_seqs)
-    return T, Hqk, H, dk, dv, N, dev, q.dtype
+    return T, Hqk, H, dk, dv, N, dev, io
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_bytes(*shape):
+    n = ctypes.c_size_t(0)
+    _check(load_library().gdr_linear_workspace_size(*shape, ctypes.byref(n)),
+           "gdr_linear_workspace_size")
+    return int(n.value)
 
 
 def gdr_linear_workspace_size(num_seqs, total_T, H_qk, H, d_k, d_v, io_dtype,
                               backward=False) -> int:
-    n = ctypes.c_size_t(0)
-    _check(load_library().gdr_linear_workspace_size(num_seqs, total_T, H_qk, H, d_k, d_v, io_dtype,
-                                                    int(backward), ctypes.byref(n)),
-           "gdr_linear_workspace_size")
-    return int(n.value)
+    return _linear_bytes(num_seqs, total_T, H_qk, H, d_k, d_v, io_dtype, int(backward))
 
 
 def gdr_linear_prefill(q, k, v, decay, initial_state=None, cu_seqlens=None, *, num_seqs=None,
@@ -661,33 +656,38 @@ def gdr_linear_prefill(q, k, v, decay, initial_state=None, cu_seqlens=None, *, n
     """
     T, Hqk, H, dk, dv, N, dev, io = _linear_args(q, k, v, decay, cu_seqlens, num_seqs)
     code = _io_code(io)
+    state = (N, H, dv, dk)
     if initial_state is not None:
-        _given(initial_state, "initial_state", (N, H, dv, dk), torch.float32, dev)
+        _given(initial_state, "initial_state", state, torch.float32, dev)
     if o is not None:
-        _given(o, "o", (T, H, dv), io, dev)
+        _given(o, "o", v.shape, io, dev)
     if final_state is not None:
-        _given(final_state, "final_state", (N, H, dv, dk), torch.float32, dev)
-    with _On(dev, stream) as on:
-        need = gdr_linear_workspace_size(N, T, Hqk, H, dk, dv, code)
-        if o is None:
-            o = torch.empty((T, H, dv), dtype=io, device=dev)
-        if final_state is None and output_final_state:
-            final_state = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev)
+        _given(final_state, "final_state", state, torch.float32, dev)
+    need = _linear_bytes(N, T, Hqk, H, dk, dv, code, 0)
+
+    def run(stream_ptr):
+        out = torch.empty_like(v) if o is None else o
+        fin = final_state
+        if fin is None and output_final_state:
+            fin = torch.empty(state, dtype=torch.float32, device=dev)
         ws, ws_bytes, _keep = _scratch(workspace, need, dev)
         st = load_library().gdr_linear_prefill(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(initial_state), _ptr(cu_seqlens), N, T,
-            Hqk, H, dk, dv, code, _ptr(o), _ptr(final_state), ws, ws_bytes, on.ptr)
-    _check(st, "gdr_linear_prefill")
-    return o, final_state
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), _at(initial_state),
+            _at(cu_seqlens), N, T, Hqk, H, dk, dv, code, out.data_ptr(), _at(fin), ws, ws_bytes,
+            stream_ptr)
+        _check(st, "gdr_linear_prefill")
+        return out, fin
+
+    return _on(dev, stream, run)
 
 
 def gdr_linear_check_workspace(workspace, stream=None):
     """Raise GdrError(GDR_ERR_DEVICE_TIMEOUT) if a bounded device-side wait of
     the call that used this workspace gave up (synchronises the stream)."""
-    with _On(workspace.device, stream) as on:
-        st = load_library().gdr_linear_check_workspace(
-            _ptr(workspace), workspace.numel() * workspace.element_size(), on.ptr)
-    _check(st, "gdr_linear_check_workspace")
+    _on(workspace.device, stream, lambda stream_ptr: _check(
+        load_library().gdr_linear_check_workspace(
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream_ptr),
+        "gdr_linear_check_workspace"))
 
 
 def gdr_linear_decode(q, k, v, decay, state, *, o=None, stream=None):
@@ -697,16 +697,20 @@ def gdr_linear_decode(q, k, v, decay, state, *, o=None, stream=None):
     [N, H, d_v, d_k] fp32.  Returns o [N, H, d_v].
     """
     N, Hqk, H, dk, dv, _, dev, io = _linear_args(q, k, v, decay, None, None)
+    code = _io_code(io)
     _given(state, "state", (N, H, dv, dk), torch.float32, dev)
     if o is not None:
-        _given(o, "o", (N, H, dv), io, dev)
-    with _On(dev, stream) as on:
-        if o is None:
-            o = torch.empty((N, H, dv), dtype=io, device=dev)
-        st = load_library().gdr_linear_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(state),
-                                              N, Hqk, H, dk, dv, _io_code(io), _ptr(o), on.ptr)
-    _check(st, "gdr_linear_decode")
-    return o
+        _given(o, "o", v.shape, io, dev)
+
+    def run(stream_ptr):
+        out = torch.empty_like(v) if o is None else o
+        st = load_library().gdr_linear_decode(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), state.data_ptr(), N, Hqk,
+            H, dk, dv, code, out.data_ptr(), stream_ptr)
+        _check(st, "gdr_linear_decode")
+        return out
+
+    return _on(dev, stream, run)
 
 
 def gdr_linear_backward(q, k, v, decay, initial_state=None, cu_seqlens=None, *, d_o,
@@ -721,42 +725,48 @@ def gdr_linear_backward(q, k, v, decay, initial_state=None, cu_seqlens=None, *, 
     """
     T, Hqk, H, dk, dv, N, dev, io = _linear_args(q, k, v, decay, cu_seqlens, num_seqs)
     code = _io_code(io)
-    _given(d_o, "d_o", (T, H, dv), io, dev)
-    for t, name in ((initial_state, "initial_state"), (d_final_state, "d_final_state")):
-        if t is not None:
-            _given(t, name, (N, H, dv, dk), torch.float32, dev)
-    with _On(dev, stream) as on:
-        need = gdr_linear_workspace_size(N, T, Hqk, H, dk, dv, code, True)
+    state = (N, H, dv, dk)
+    _given(d_o, "d_o", v.shape, io, dev)
+    if initial_state is not None:
+        _given(initial_state, "initial_state", state, torch.float32, dev)
+    if d_final_state is not None:
+        _given(d_final_state, "d_final_state", state, torch.float32, dev)
+    need = _linear_bytes(N, T, Hqk, H, dk, dv, code, 1)
+
+    def run(stream_ptr):
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        dh0 = (torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev)
+        dh0 = (torch.empty(state, dtype=torch.float32, device=dev)
                if want_d_initial_state else None)
         ws, ws_bytes, _keep = _scratch(workspace, need, dev)
         st = load_library().gdr_linear_backward(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(initial_state), _ptr(cu_seqlens), N, T,
-            Hqk, H, dk, dv, code, _ptr(d_o), _ptr(d_final_state), _ptr(dq), _ptr(dk_), _ptr(dv_),
-            _ptr(dh0), ws, ws_bytes, on.ptr)
-    _check(st, "gdr_linear_backward")
-    return dq, dk_, dv_, dh0
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), _at(initial_state),
+            _at(cu_seqlens), N, T, Hqk, H, dk, dv, code, d_o.data_ptr(), _at(d_final_state),
+            dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(), _at(dh0), ws, ws_bytes, stream_ptr)
+        _check(st, "gdr_linear_backward")
+        return dq, dk_, dv_, dh0
+
+    return _on(dev, stream, run)
 
 
 def _norm_args(x, weight, gate, residual, next_weight, activation):
-    """Checks what the norm's two calls share; returns (rows, dim, device, dtype, activation)."""
+    """Checks what the norm's two calls share; returns (rows, dim, device, shape, activation)."""
     _need(x, "x")
-    if x.dim() < 1:
+    shape = x.shape
+    if len(shape) < 1:
         raise ValueError("x must have at least one dim")
-    if activation not in _ACTIVATIONS:
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, got {activation!r}")
-    dim, dev, shape = x.shape[-1], x.device, tuple(x.shape)
-    for t, name in ((gate, "gate"), (residual, "residual")):
-        if t is not None:
-            _given(t, name, shape, x.dtype, dev)
-    for t, name in ((weight, "weight"), (next_weight, "next_weight")):
-        if t is not None:
-            _given(t, name, (dim,), torch.float32, dev)
-    rows = 1
-    for n in shape[:-1]:
-        rows *= n
-    return rows, dim, dev, shape, _ACTIVATIONS[activation]
+    dim, dev, io = shape[-1], x.device, x.dtype
+    if gate is not None:
+        _given(gate, "gate", shape, io, dev)
+    if residual is not None:
+        _given(residual, "residual", shape, io, dev)
+    if weight is not None:
+        _given(weight, "weight", (dim,), torch.float32, dev)
+    if next_weight is not None:
+        _given(next_weight, "next_weight", (dim,), torch.float32, dev)
+    return x.numel() // dim if dim else 0, dim, dev, shape, act
 
 
 def gdr_norm_gate(x, weight=None, gate=None, residual=None, next_weight=None, *, scale=1.0,
@@ -770,29 +780,38 @@ def gdr_norm_gate(x, weight=None, gate=None, residual=None, next_weight=None, *,
     without next_weight.
     """
     rows, dim, dev, shape, act = _norm_args(x, weight, gate, residual, next_weight, activation)
+    code = _io_code(x.dtype)
     if y is not None:
         _given(y, "y", shape, x.dtype, dev)
     if y_norm is not None:
         if next_weight is None:
             raise ValueError("y_norm needs next_weight")
         _given(y_norm, "y_norm", shape, x.dtype, dev)
-    with _On(dev, stream) as on:
-        if y is None:
-            y = torch.empty(shape, dtype=x.dtype, device=dev)
-        if y_norm is None and next_weight is not None:
-            y_norm = torch.empty(shape, dtype=x.dtype, device=dev)
+
+    def run(stream_ptr):
+        out = torch.empty_like(x) if y is None else y
+        normed = y_norm
+        if normed is None and next_weight is not None:
+            normed = torch.empty_like(x)
         st = load_library().gdr_norm_gate(
-            _ptr(x), _ptr(weight), _ptr(gate), _ptr(residual), _ptr(next_weight), rows, dim,
-            float(scale), float(eps), act, _io_code(x.dtype), _ptr(y), _ptr(y_norm), on.ptr)
-    _check(st, "gdr_norm_gate")
-    return y, y_norm
+            x.data_ptr(), _at(weight), _at(gate), _at(residual), _at(next_weight), rows, dim,
+            float(scale), float(eps), act, code, out.data_ptr(), _at(normed), stream_ptr)
+        _check(st, "gdr_norm_gate")
+        return out, normed
+
+    return _on(dev, stream, run)
 
 
-def gdr_norm_gate_workspace_size(rows, dim) -> int:
+@functools.lru_cache(maxsize=1024)
+def _norm_bytes(rows, dim):
     n = ctypes.c_size_t(0)
     _check(load_library().gdr_norm_gate_workspace_size(rows, dim, ctypes.byref(n)),
            "gdr_norm_gate_workspace_size")
     return int(n.value)
+
+
+def gdr_norm_gate_workspace_size(rows, dim) -> int:
+    return _norm_bytes(rows, dim)
 
 
 def gdr_norm_gate_backward(x, dy=None, dn=None, weight=None, gate=None, residual=None,
@@ -805,22 +824,27 @@ def gdr_norm_gate_backward(x, dy=None, dn=None, weight=None, gate=None, residual
     without dn.
     """
     rows, dim, dev, shape, act = _norm_args(x, weight, gate, residual, next_weight, activation)
+    code = _io_code(x.dtype)
     if dy is None and dn is None:
         raise ValueError("dy or dn is required")
-    for t, name in ((dy, "dy"), (dn, "dn")):
-        if t is not None:
-            _given(t, name, shape, x.dtype, dev)
-    if dn is not None and next_weight is None:
-        raise ValueError("dn needs next_weight")
-    with _On(dev, stream) as on:
+    if dy is not None:
+        _given(dy, "dy", shape, x.dtype, dev)
+    if dn is not None:
+        _given(dn, "dn", shape, x.dtype, dev)
+        if next_weight is None:
+            raise ValueError("dn needs next_weight")
+    need = 0 if weight is None and dn is None else _norm_bytes(rows, dim)
+
+    def run(stream_ptr):
         new = lambda like: None if like is None else torch.empty_like(like)  # noqa: E731
         dx, dweight, dgate, dres = new(x), new(weight), new(gate), new(residual)
         dnext = new(next_weight) if dn is not None else None
-        need = 0 if dweight is None and dnext is None else gdr_norm_gate_workspace_size(rows, dim)
         ws, ws_bytes, _keep = _scratch(workspace, need, dev)
         st = load_library().gdr_norm_gate_backward(
-            _ptr(x), _ptr(weight), _ptr(gate), _ptr(residual), _ptr(next_weight), rows, dim,
-            float(scale), float(eps), act, _io_code(x.dtype), _ptr(dy), _ptr(dn), _ptr(dx),
-            _ptr(dweight), _ptr(dgate), _ptr(dres), _ptr(dnext), ws, ws_bytes, on.ptr)
-    _check(st, "gdr_norm_gate_backward")
-    return dx, dweight, dgate, dres, dnext
+            x.data_ptr(), _at(weight), _at(gate), _at(residual), _at(next_weight), rows, dim,
+            float(scale), float(eps), act, code, _at(dy), _at(dn), dx.data_ptr(), _at(dweight),
+            _at(dgate), _at(dres), _at(dnext), ws, ws_bytes, stream_ptr)
+        _check(st, "gdr_norm_gate_backward")
+        return dx, dweight, dgate, dres, dnext
+
+    return _on(dev, stream, run)
