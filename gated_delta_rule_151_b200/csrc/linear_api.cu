@@ -1,6 +1,7 @@
 // C ABI of linear attention with a decay for each head: argument checks, the
 // plan (how sequences are cut into segments), workspace layout and launches.
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "api_common.h"
@@ -26,54 +27,75 @@ struct Plan {
     int seg_tokens, slots, inner;
 };
 
-// Cost of a 64-token block of one head in the output and the state pass, and
-// what a CTA and the pass between segments cost beside, in microseconds, with
-// `at_once` CTAs resident on the GPU.
+// Measured costs, in microseconds, of a 64-token block of one head in the output and
+// in the state pass: alone on an SM, and the SM's time for it among others.  The
+// tensor-core CTAs have an SM to themselves; several of the others share one.
 struct Costs {
-    int at_once;
-    double block, state, cta, join;
+    bool exclusive;
+    double out_alone, out_shared, state_alone, state_shared;
+    double cta, join;   // beside: a CTA's start and end; the pass between segments
 };
 
 bool tensor_cores(int d_k, int d_v, bool bf16) { return bf16 && d_k == 128 && d_v == 128; }
 
-Costs costs_of(int d_b, int d_v, bool bf16) {
-    if (tensor_cores(d_b, d_v, bf16)) return Costs{kSMs, 1.6, 1.0, 5.0, 4.0};
-    return Costs{kSMs * 2, 0.06 * d_b + 2.0, 0.04 * d_b + 2.0, 3.0, 4.0};
+Costs costs_of(int d_k, int d_v, bool bf16) {
+    if (tensor_cores(d_k, d_v, bf16)) return Costs{true, 1.6, 1.6, 0.9, 0.9, 4.0, 5.0};
+    const double x = (double)d_k * d_v / 16384;
+    return Costs{false, 9 + 28 * x, 29 * x, 4 + 10 * x, 12 * x, 3.0, 4.0};
 }
 
-// Equal lengths: the segment length whose passes end first by the costs above,
-// one wave of segments after another.  Packed lengths are not known here:
-// about two segments for every place on the GPU bound what one long sequence
-// can cost, and shorter sequences stay whole.
-Plan make_plan(int N, int total_T, int H, int d_b, int d_v, bool bf16, bool equal) {
-    const Costs c = costs_of(d_b, d_v, bf16);
-    Plan p;
-    if (!equal) {
-        const int64_t blocks = ((int64_t)total_T + kScanBlock - 1) / kScanBlock;
-        const int64_t per = std::max<int64_t>(8, (blocks * H + 2 * c.at_once - 1) / (2 * c.at_once));
-        p.seg_tokens = (int)std::min<int64_t>(per, INT32_MAX / kScanBlock) * kScanBlock;
-        p.inner = total_T / p.seg_tokens;
-        p.slots = N + p.inner;
-        return p;
-    }
+// A pass over `items` segments of at most `blocks` blocks, `work` blocks in all.
+double pass_time(const Costs &c, double items, double blocks, double work, double alone, double shared, bool even) {
+    const double one = blocks * alone + c.cta;
+    if (c.exclusive && even) return std::ceil(items / kSMs) * one;
+    if (items <= kSMs) return one;
+    const double tail = even ? 0 : 0.5 * one;    // unequal segments end at different times
+    return std::max(one, (work * shared + (c.exclusive ? items * c.cta : 0)) / kSMs + tail);
+}
+
+// The segment length whose passes end first by these costs.  Packed lengths are not
+// known here: they are taken to lie around their mean, up to twice of it, so that
+// with a segment below that some sequences are cut.
+Plan make_plan(int N, int total_T, int H, int d_k, int d_v, bool bf16, bool equal) {
+    const Costs c = costs_of(d_k, d_v, bf16);
+    const double state_bytes = (double)H * d_k * d_v * 4, most_bytes = 128e6;
     const int len = total_T / N;
-    const int64_t blocks = std::max(1, (len + kScanBlock - 1) / kScanBlock), chains = (int64_t)N * H;
-    auto waves = [&](int64_t items) { return (double)((items + c.at_once - 1) / c.at_once); };
-    int64_t best = blocks;
-    double least = waves(chains) * (blocks * c.block + c.cta);
-    for (int64_t segs = 2; segs <= std::min<int64_t>(blocks, 2 * c.at_once); ++segs) {
-        const int64_t per = (blocks + segs - 1) / segs, n = (blocks + per - 1) / per;
-        const double t = waves(chains * (n - 1)) * (per * c.state + c.cta) +
-                         waves(chains * n) * (per * c.block + c.cta) + c.join;
+    const int64_t total = std::max<int64_t>(1, ((int64_t)total_T + kScanBlock - 1) / kScanBlock);
+    const int64_t own = std::max(1, (len + kScanBlock - 1) / kScanBlock);         // blocks of an equal sequence
+    const int64_t longest = equal ? own : std::min<int64_t>(total, 2 * ((total + N - 1) / N));
+    const double work = (double)(equal ? own * N : total) * H;
+    auto segments = [&](int64_t per) -> double {
+        return equal ? (double)N * ((own + per - 1) / per) : per >= longest ? N : (double)total / per + 0.5 * N;
+    };
+    int64_t best = longest;
+    double least = pass_time(c, (double)N * H, (double)longest, work, c.out_alone, c.out_shared, equal);
+    for (int64_t per = 1; per < longest; per += per < 64 ? 1 : per / 32) {
+        const double all = segments(per), inner = std::max(0.0, all - N);
+        if (inner * state_bytes > most_bytes) continue;
+        const double t = pass_time(c, inner * H, (double)per, inner * H * per, c.state_alone, c.state_shared, equal) +
+                         pass_time(c, all * H, (double)per, work, c.out_alone, c.out_shared, equal) + c.join +
+                         inner * state_bytes / 1.5e6;    // the join reads and writes them: 3 TB/s
         if (t < least) {
             least = t;
             best = per;
         }
     }
-    const int64_t n = (blocks + best - 1) / best;
-    p.seg_tokens = (int)best * kScanBlock;
-    p.slots = (int)(N * n);
-    p.inner = (int)(N * (n - 1));
+    if (!equal) {
+        // a sequence far beyond the assumed lengths is cut all the same, as finely as the
+        // states fit
+        if (best == longest) best = std::max<int64_t>(2 * longest, 16);
+        best = std::max<int64_t>(best, (int64_t)std::ceil((double)total * state_bytes / most_bytes));
+    }
+    Plan p;
+    p.seg_tokens = (int)std::min<int64_t>(best, INT32_MAX / kScanBlock) * kScanBlock;
+    if (equal) {
+        const int n = segments_of(len, p.seg_tokens);
+        p.slots = N * n;
+        p.inner = N * (n - 1);
+    } else {
+        p.inner = total_T / p.seg_tokens;
+        p.slots = N + p.inner;
+    }
     return p;
 }
 

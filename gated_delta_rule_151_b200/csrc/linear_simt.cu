@@ -1,20 +1,25 @@
 // Linear attention with a decay for each head on the CUDA cores (fp32 or bf16
 // inputs, any served d), the passes between segments, and the decode step.
 //
-// The scan of linear_common.cuh runs token by token with one state row per
-// thread, in registers: S_r <- x S_r + v_r b, o_r = S_r . a (reverse: the decay
-// comes after the output instead of before the update).  A row needs no other
-// row, so there is no reduction across threads, and at d = 128 the 3 d_b
-// operations per row and token are about what the blocked form costs without
-// tensor cores.  a, b and v of eight tokens at a time are staged in shared
-// memory as fp32 (every thread reads the same a and b: broadcasts); the next
-// eight are fetched meanwhile.  The arithmetic is fp32 throughout.
+// The scan of linear_common.cuh in tiles of eight tokens, all in fp32.  With u and
+// j the places of a tile of n tokens in scan order and x = e^g,
+//
+//     o_u = x^{u+1-r} S a_u + sum_{j<=u} x^{u-j} (a_u . b_j) v_j
+//     S  <- x^n S + sum_j x^{n-1+r-j} v_j b_j^T
+//
+// The state stays in registers: a thread has 32 columns (every SPL-th group of
+// four) of two rows, so that each 16 bytes of a or b read from shared memory
+// meet four packed products, and eight outputs run side by side.  The 36 dots
+// a_u . b_j of a tile are made one tile ahead by a few of the threads; a, b and v
+// of the tile after that are on their way in registers.  One barrier a tile.
+// Against a loop over single tokens this takes two products a state element and
+// token instead of three, and rounds the state once a tile.
 #include "linear_common.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr int kTok = 8;   // tokens per stage
+constexpr int kTok = 8;   // tokens of a tile
 
 __device__ __forceinline__ float4 load4f(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ float4 load4f(const __nv_bfloat16 *p) {
@@ -23,14 +28,26 @@ __device__ __forceinline__ float4 load4f(const __nv_bfloat16 *p) {
                        __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
 }
 
+template <int DB, int DV>
+struct Tiling {
+    static constexpr int COLS = DB < 32 ? DB : 32;    // columns of a thread
+    static constexpr int SPL = DB / COLS;             // threads of a row
+    static constexpr int RT = DV / 2;                 // its rows: r and r + RT
+    static constexpr int USED = RT * SPL;
+    static constexpr int NT = USED < 32 ? 32 : USED;
+    static constexpr int LD = DB + 4;                 // row stride of a and b: eight rows cover all banks
+};
+
 template <int DB, int DV, bool OUT, bool REV, typename In, typename Out>
-__global__ void __launch_bounds__(DV < 32 ? 32 : DV)
+__global__ void __launch_bounds__(Tiling<DB, DV>::NT)
 scan_simt_kernel(const ScanArgs p) {
-    constexpr int NT = DV < 32 ? 32 : DV;
-    constexpr int ROWS = OUT ? 2 * DB + DV : DB + DV;      // floats per staged token: b, v, a
-    constexpr int VECS = kTok * ROWS / 4;                  // float4 per stage
-    constexpr int PER = (VECS + NT - 1) / NT;
-    __shared__ __align__(16) float tile[2][kTok * ROWS];
+    using Ti = Tiling<DB, DV>;
+    constexpr int NT = Ti::NT, SPL = Ti::SPL, RT = Ti::RT, LD = Ti::LD, M = Ti::COLS / 4;
+    constexpr int ROW = DB + DV + (OUT ? DB : 0);          // floats of a token: b, v, a
+    constexpr int PER = (kTok * ROW / 4 + NT - 1) / NT;    // of their groups of four, for each thread
+    __shared__ __align__(16) float sb[3][kTok][LD], sa[OUT ? 3 : 1][OUT ? kTok : 1][LD], sv[3][kTok][DV];
+    __shared__ __align__(16) float dots[2][kTok][kTok];
+    __shared__ float pw[kTok + 2];
     __shared__ int scratch[34];
     const int tid = threadIdx.x;
     const int slot = blockIdx.x / p.H, h = blockIdx.x % p.H;
@@ -41,119 +58,195 @@ scan_simt_kernel(const ScanArgs p) {
     if (seg.n < 0) return;
     const bool last = seg.index == seg.count - 1;
     const int ha = h / (p.H / p.HA), hb = h / (p.H / p.HB), hv = h / (p.H / p.HV);
-    const float decay = expf(clamp_log_gate(p.decay[h]));
-    const float2 x2 = make_float2(decay, decay);
-    const bool row = tid < DV;
+    if (tid <= kTok) pw[tid] = expf(clamp_log_gate(p.decay[h]) * (float)tid);
+    const bool used = tid < Ti::USED;
+    const int split = tid % SPL, r0 = used ? tid / SPL : 0, r1 = r0 + RT;
     const size_t state_at = ((size_t)seg.n * p.H + h) * (DV * DB);
 
-    float2 S[DB / 2];
+    float2 S[2][2 * M];
 #pragma unroll
-    for (int i = 0; i < DB / 2; ++i) S[i] = make_float2(0.f, 0.f);
-    if (row) {
-        if (OUT && seg.index > 0) {
-            const float4 *src = reinterpret_cast<const float4 *>(
-                p.seg + ((size_t)(seg.state - 1) * p.H + h) * (DV * DB)) + tid;
+    for (int i = 0; i < 2 * M; ++i) S[0][i] = S[1][i] = make_float2(0.f, 0.f);
+    // a row's float4 number m of this thread is number split + SPL m of the row
+    auto each = [&](auto f) {
 #pragma unroll
-            for (int i = 0; i < DB / 4; ++i) {
-                const float4 x = src[i * DV];
-                S[2 * i] = make_float2(x.x, x.y);
-                S[2 * i + 1] = make_float2(x.z, x.w);
-            }
-        } else if (seg.index == 0 && p.s_in != nullptr && p.turned) {
-            const float *src = p.s_in + state_at + tid;
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int i = 0; i < DB / 2; ++i) S[i] = make_float2(src[2 * i * DV], src[(2 * i + 1) * DV]);
-        } else if (seg.index == 0 && p.s_in != nullptr) {
-            const float4 *src = reinterpret_cast<const float4 *>(p.s_in + state_at + (size_t)tid * DB);
-#pragma unroll
-            for (int i = 0; i < DB / 4; ++i) {
-                const float4 x = src[i];
-                S[2 * i] = make_float2(x.x, x.y);
-                S[2 * i + 1] = make_float2(x.z, x.w);
-            }
-        }
+            for (int m = 0; m < M; ++m) f(q, m, q == 0 ? r0 : r1, split + SPL * m);
+    };
+    if (used && OUT && seg.index > 0) {
+        const float4 *src = reinterpret_cast<const float4 *>(p.seg + ((size_t)(seg.state - 1) * p.H + h) * (DV * DB));
+        each([&](int q, int m, int r, int c) {
+            const float4 x = src[r * (DB / 4) + c];
+            S[q][2 * m] = make_float2(x.x, x.y);
+            S[q][2 * m + 1] = make_float2(x.z, x.w);
+        });
+    } else if (used && seg.index == 0 && p.s_in != nullptr) {
+        const float *src = p.s_in + state_at;
+        each([&](int q, int m, int r, int c) {
+            float4 x;
+            if (p.turned) x = make_float4(src[(4 * c) * DV + r], src[(4 * c + 1) * DV + r], src[(4 * c + 2) * DV + r], src[(4 * c + 3) * DV + r]);
+            else x = reinterpret_cast<const float4 *>(src)[r * (DB / 4) + c];
+            S[q][2 * m] = make_float2(x.x, x.y);
+            S[q][2 * m + 1] = make_float2(x.z, x.w);
+        });
     }
 
-    // token u of the scan, and element e (a multiple of 4) of its staged row
+    // place u of the scan, and element e (a multiple of 4) of its token's b, v, a
     auto token = [&](int u) { return (size_t)(seg.t0 + (REV ? seg.len - 1 - u : u)); };
-    auto fetch = [&](int u, int e) {
-        const size_t t = token(u);
-        if (e < DB) return load4f(static_cast<const In *>(p.b) + (t * p.HB + hb) * DB + e);
-        if (e < DB + DV) return load4f(static_cast<const In *>(p.v) + (t * p.HV + hv) * DV + (e - DB));
-        return load4f(static_cast<const In *>(p.a) + (t * p.HA + ha) * DB + (e - DB - DV));
-    };
+    // what this thread fetches of a tile: where its groups lie in the first one, and how
+    // far the next tile's are
     float4 next[PER];
-    auto fetch_all = [&](int u0) {
+    const In *src[PER];
+    int64_t step[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int at = (i * NT + tid) * 4, u = u0 + at / ROWS;
-            next[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (at < kTok * ROWS && u < seg.len) next[i] = fetch(u, at % ROWS);
-        }
-    };
-    if (seg.len > 0) fetch_all(0);
-    for (int u0 = 0, buf = 0; u0 < seg.len; u0 += kTok, buf ^= 1) {
+    for (int i = 0; i < PER; ++i) {
+        const int at = (i * NT + tid) * 4, u = at / ROW, e = at % ROW;
+        const int64_t t = seg.t0 + (REV ? seg.len - 1 - u : u);
+        const int64_t heads = e < DB ? (int64_t)p.HB * DB : e < DB + DV ? (int64_t)p.HV * DV : (int64_t)p.HA * DB;
+        const In *from = e < DB ? static_cast<const In *>(p.b) + hb * DB + e
+                       : e < DB + DV ? static_cast<const In *>(p.v) + hv * DV + (e - DB)
+                                     : static_cast<const In *>(p.a) + ha * DB + (e - DB - DV);
+        src[i] = from + t * heads;
+        step[i] = (REV ? -kTok : kTok) * heads;
+    }
+    auto fetch = [&](int u0) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int at = (i * NT + tid) * 4;
-            if (at < kTok * ROWS) *reinterpret_cast<float4 *>(&tile[buf][at]) = next[i];
+            next[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (at < kTok * ROW && u0 + at / ROW < seg.len) next[i] = load4f(src[i]);
+            src[i] += step[i];
         }
-        __syncthreads();
-        if (u0 + kTok < seg.len) fetch_all(u0 + kTok);
-        const int n = min(kTok, seg.len - u0);
-        if (row) {
-            for (int u = 0; u < n; ++u) {
-                const float *t = &tile[buf][u * ROWS];
-                const float4 *b4 = reinterpret_cast<const float4 *>(t);
-                const float4 *a4 = reinterpret_cast<const float4 *>(t + DB + DV);
-                const float v = t[DB + tid];
-                const float2 v2 = make_float2(v, v);
-                float2 o0 = make_float2(0.f, 0.f), o1 = o0;
+    };
+    auto put = [&](int buf) {
 #pragma unroll
-                for (int i = 0; i < DB / 4; ++i) {
-                    const float4 b = b4[i];
-                    float2 s0 = S[2 * i], s1 = S[2 * i + 1];
-                    if (!REV) {
-                        s0 = __fmul2_rn(s0, x2);
-                        s1 = __fmul2_rn(s1, x2);
-                    }
-                    s0 = __ffma2_rn(v2, make_float2(b.x, b.y), s0);
-                    s1 = __ffma2_rn(v2, make_float2(b.z, b.w), s1);
-                    if (OUT) {
-                        const float4 a = a4[i];
-                        o0 = __ffma2_rn(s0, make_float2(a.x, a.y), o0);
-                        o1 = __ffma2_rn(s1, make_float2(a.z, a.w), o1);
-                    }
-                    if (REV) {
-                        s0 = __fmul2_rn(s0, x2);
-                        s1 = __fmul2_rn(s1, x2);
-                    }
-                    S[2 * i] = s0;
-                    S[2 * i + 1] = s1;
+        for (int i = 0; i < PER; ++i) {
+            const int at = (i * NT + tid) * 4, u = at / ROW, e = at % ROW;
+            if (at >= kTok * ROW) continue;
+            float *dst = e < DB ? &sb[buf][u][e] : e < DB + DV ? &sv[buf][u][e - DB] : &sa[OUT ? buf : 0][OUT ? u : 0][e - DB - DV];
+            *reinterpret_cast<float4 *>(dst) = next[i];
+        }
+    };
+    auto make_dots = [&](int buf, int to) {
+        for (int i = tid; i < kTok * kTok; i += NT) {
+            const int u = i / kTok, j = i % kTok;
+            if (j > u) continue;
+            float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+#pragma unroll 8
+            for (int c = 0; c < DB; c += 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(&sa[OUT ? buf : 0][OUT ? u : 0][c]);
+                const float4 b = *reinterpret_cast<const float4 *>(&sb[buf][j][c]);
+                s0 = __ffma2_rn(make_float2(a.x, a.y), make_float2(b.x, b.y), s0);
+                s1 = __ffma2_rn(make_float2(a.z, a.w), make_float2(b.z, b.w), s1);
+            }
+            dots[to][u][j] = ((s0.x + s0.y) + (s1.x + s1.y)) * pw[u - j];
+        }
+    };
+    const int tiles = (seg.len + kTok - 1) / kTok;
+    if (tiles > 0) {
+        fetch(0);
+        put(0);
+        fetch(kTok);
+        __syncthreads();
+        if (OUT) make_dots(0, 0);
+    }
+    for (int k = 0, buf = 0; k < tiles; ++k) {
+        const int after = buf == 2 ? 0 : buf + 1, n = min(kTok, seg.len - k * kTok);
+        put(after);
+        __syncthreads();
+        if (k + 1 < tiles) {
+            fetch((k + 2) * kTok);
+            if (OUT) make_dots(after, (k + 1) & 1);
+        }
+        float v[2][kTok];
+#pragma unroll
+        for (int j = 0; j < kTok; ++j) {
+            v[0][j] = sv[buf][j][r0];
+            v[1][j] = sv[buf][j][r1];
+        }
+        if (OUT) {
+            float2 acc[2][kTok];
+#pragma unroll
+            for (int u = 0; u < kTok; ++u) acc[0][u] = acc[1][u] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int u = 0; u < kTok; ++u) {
+                    const float4 a = *reinterpret_cast<const float4 *>(&sa[OUT ? buf : 0][OUT ? u : 0][4 * (split + SPL * m)]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        acc[q][u] = __ffma2_rn(S[q][2 * m + 1], make_float2(a.z, a.w),
+                                               __ffma2_rn(S[q][2 * m], make_float2(a.x, a.y), acc[q][u]));
                 }
-                if (OUT)
-                    store_io(static_cast<Out *>(p.out) + (token(u0 + u) * p.H + h) * DV + tid,
-                             (o0.x + o0.y) + (o1.x + o1.y));
+            // the row's threads add up; each stores every SPL-th token
+            Out *dst = static_cast<Out *>(p.out) + (token(k * kTok) * p.H + h) * DV;
+            const int64_t row = REV ? -(int64_t)p.H * DV : (int64_t)p.H * DV;
+#pragma unroll
+            for (int u = 0; u < kTok; ++u) {
+                float o[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    o[q] = acc[q][u].x + acc[q][u].y;
+#pragma unroll
+                    for (int off = SPL / 2; off > 0; off >>= 1) o[q] += __shfl_xor_sync(0xffffffffu, o[q], off);
+                    o[q] *= pw[REV ? u : u + 1];
+                }
+#pragma unroll
+                for (int j = 0; j <= u; j += 4) {
+                    const float4 w = *reinterpret_cast<const float4 *>(&dots[k & 1][u][j]);
+                    const float ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (j + e <= u) {
+                            o[0] = fmaf(ws[e], v[0][j + e], o[0]);
+                            o[1] = fmaf(ws[e], v[1][j + e], o[1]);
+                        }
+                }
+                if (used && u % SPL == split && u < n) {
+                    store_io(dst + u * row + r0, o[0]);
+                    store_io(dst + u * row + r1, o[1]);
+                }
             }
         }
-    }
-    if (row && !OUT) {
-        float4 *dst = reinterpret_cast<float4 *>(p.seg + ((size_t)seg.state * p.H + h) * (DV * DB)) + tid;
 #pragma unroll
-        for (int i = 0; i < DB / 4; ++i)
-            dst[i * DV] = make_float4(S[2 * i].x, S[2 * i].y, S[2 * i + 1].x, S[2 * i + 1].y);
-    }
-    if (row && OUT && last && p.s_out != nullptr) {
-        float4 *dst = reinterpret_cast<float4 *>(p.s_out + state_at + (size_t)tid * DB);
+        for (int j = 0; j < kTok; ++j) {
+            const float w = pw[max(n - 1 - j, 0) + (REV ? 1 : 0)];      // (the tokens behind n are zeros)
+            v[0][j] *= w;
+            v[1][j] *= w;
+        }
+        const float2 xn = make_float2(pw[n], pw[n]);
 #pragma unroll
-        for (int i = 0; i < DB / 4; ++i)
-            dst[i] = make_float4(S[2 * i].x, S[2 * i].y, S[2 * i + 1].x, S[2 * i + 1].y);
+        for (int m = 0; m < M; ++m) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                S[q][2 * m] = __fmul2_rn(S[q][2 * m], xn);
+                S[q][2 * m + 1] = __fmul2_rn(S[q][2 * m + 1], xn);
+            }
+#pragma unroll
+            for (int j = 0; j < kTok; ++j) {
+                const float4 b = *reinterpret_cast<const float4 *>(&sb[buf][j][4 * (split + SPL * m)]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float2 w = make_float2(v[q][j], v[q][j]);
+                    S[q][2 * m] = __ffma2_rn(w, make_float2(b.x, b.y), S[q][2 * m]);
+                    S[q][2 * m + 1] = __ffma2_rn(w, make_float2(b.z, b.w), S[q][2 * m + 1]);
+                }
+            }
+        }
+        buf = after;
+    }
+    float *out_state = OUT ? (last ? p.s_out : nullptr) : p.seg;
+    if (used && out_state != nullptr) {
+        float4 *dst = reinterpret_cast<float4 *>(out_state + (OUT ? state_at : ((size_t)seg.state * p.H + h) * (DV * DB)));
+        each([&](int q, int m, int r, int c) {
+            dst[r * (DB / 4) + c] = make_float4(S[q][2 * m].x, S[q][2 * m].y, S[q][2 * m + 1].x, S[q][2 * m + 1].y);
+        });
     }
 }
 
 template <int DB, int DV, typename In, typename Out>
 cudaError_t launch_shape(const ScanArgs &p, bool reverse, bool states, bool after, cudaStream_t s) {
-    constexpr int NT = DV < 32 ? 32 : DV;
+    constexpr int NT = Tiling<DB, DV>::NT;
     const unsigned grid = (unsigned)(states ? p.inner : p.slots) * p.H;
     if (states)
         return reverse ? launch_kernel(after, scan_simt_kernel<DB, DV, false, true, In, In>, grid, NT, 0, s, p)
