@@ -100,9 +100,10 @@ Plan make_plan(int N, int total_T, int H, int d_k, int d_v, bool bf16, bool equa
 }
 
 // Workspace of one call: header, status words of every pass, a copy of the
-// incoming state, the states between segments, fp32 partial gradients.
+// incoming state, the states between segments (forward scan, reverse scan), fp32
+// partial gradients.
 struct Layout {
-    size_t status, copy, seg, part, total;
+    size_t status, copy, seg[2], part, total;
     uint32_t words;
 };
 
@@ -110,11 +111,12 @@ Layout make_layout(const Plan &p, int N, int total_T, int H_qk, int H, int d_k, 
                    bool backward) {
     Layout l;
     const size_t state = (size_t)H * d_k * d_v * 4;
-    l.words = (uint32_t)((size_t)(p.slots + p.inner) * H * (backward ? 3 : 1));
+    l.words = (uint32_t)((size_t)(backward ? 3 * p.slots + 2 * p.inner : p.slots + p.inner) * H);
     l.status = kHeader;
     l.copy = l.status + up256((size_t)l.words * 4);
-    l.seg = l.copy + (p.inner > 0 && !backward ? up256(N * state) : 0);
-    l.part = l.seg + up256(p.inner * state);
+    l.seg[0] = l.copy + (p.inner > 0 && !backward ? up256(N * state) : 0);
+    l.seg[1] = l.seg[0] + up256(p.inner * state);
+    l.part = l.seg[1] + (backward ? up256(p.inner * state) : 0);
     l.total = l.part + (backward && H != H_qk ? up256((size_t)total_T * H * d_k * 4) : 0);
     return l;
 }
@@ -142,20 +144,21 @@ struct Call {
     cudaStream_t stream;
     uint32_t used;   // status words handed out
     bool launched;   // a kernel of this call went before
+    cudaError_t error;
 
-    cudaError_t scan(const void *a, int HA, const void *b, int HB, const void *v, int HV, int d_b,
-                     int d_v, const float *s_in, bool turned, float *s_out, void *out, bool out_f32,
-                     bool reverse) {
+    // A scan's arguments; `buffer`: which states between segments it goes by.
+    ScanArgs args(const void *a, int HA, const void *b, int HB, const void *v, int HV, const float *s_in,
+                  bool turned, float *s_out, void *out, int buffer, bool seg_turned) const {
         ScanArgs p;
         p.a = a; p.b = b; p.v = v;
         p.out = out;
         p.decay = decay;
         p.s_in = s_in;
         p.s_out = s_out;
-        p.seg = reinterpret_cast<float *>(ws + lay.seg);
+        p.seg = reinterpret_cast<float *>(ws + lay.seg[buffer]);
         p.header = reinterpret_cast<uint32_t *>(ws);
-        p.status = reinterpret_cast<uint32_t *>(ws + lay.status) + used;
-        p.status_words = tensor_cores(d_b, d_v, bf16) ? lay.words : 0;
+        p.status = nullptr;
+        p.status_words = 0;
         p.cu = cu;
         p.N = N; p.total_T = total_T; p.H = H;
         p.HA = HA; p.HB = HB; p.HV = HV;
@@ -163,24 +166,28 @@ struct Call {
         p.slots = plan.slots;
         p.inner = plan.inner;
         p.turned = turned;
-        cudaError_t e = cudaSuccess;
-        if (plan.inner > 0) {
-            e = pass(p, d_b, d_v, reverse, true, out_f32);
-            // (of two segments the first one's own state is what the second starts from)
-            if (e == cudaSuccess && (cu != nullptr || plan.inner > N))
-                e = launch_scan_join(p, d_b * d_v, reverse, stream);
-            p.status += (size_t)plan.inner * H;
-        }
-        if (e == cudaSuccess) e = pass(p, d_b, d_v, reverse, false, out_f32);
-        used += (uint32_t)(plan.slots + plan.inner) * H;
-        return e;
+        p.seg_turned = seg_turned;
+        return p;
     }
 
-    cudaError_t pass(const ScanArgs &p, int d_b, int d_v, bool reverse, bool states, bool out_f32) {
-        const bool after = launched;
+    // One pass, and the pass between segments; nothing after an error.
+    void pass(ScanArgs p, int d_b, int d_v, bool reverse, bool states, bool out_f32) {
+        if (error != cudaSuccess || (states && plan.inner == 0)) return;
+        const bool tc = tensor_cores(d_b, d_v, bf16);
+        p.status = reinterpret_cast<uint32_t *>(ws + lay.status) + used;
+        p.status_words = tc ? lay.words : 0;
+        used += (uint32_t)(states ? plan.inner : plan.slots) * H;
+        error = tc ? launch_scan_tc(p, reverse, states, out_f32, launched, stream)
+                   : launch_scan_simt(p, d_b, d_v, reverse, states, bf16, out_f32, launched, stream);
         launched = true;
-        if (tensor_cores(d_b, d_v, bf16)) return launch_scan_tc(p, reverse, states, out_f32, after, stream);
-        return launch_scan_simt(p, d_b, d_v, reverse, states, bf16, out_f32, after, stream);
+    }
+    void join(const ScanArgs &p, int d_b, int d_v, bool reverse) {
+        // (of two segments the first one's own state is what the second starts from)
+        if (error != cudaSuccess || plan.inner == 0 || (cu == nullptr && plan.inner == N)) return;
+        error = launch_scan_join(p, d_b * d_v, reverse, stream);
+    }
+    void sum(const float *part, int H_qk, int d, void *out) {
+        if (error == cudaSuccess && H != H_qk) error = launch_group_sum(part, total_T, H_qk, H / H_qk, d, bf16, out, stream);
     }
 };
 
@@ -254,7 +261,7 @@ gdr_status_t gdr_linear_prefill(const void *q, const void *k, const void *v, con
     if (total_T == 0) return status_of(pass_state(final_state, initial_state, state, s));
 
     Call c{cu_seqlens, decay, num_seqs, total_T, H, plan, lay, static_cast<uint8_t *>(workspace),
-           io_dtype == GDR_BF16, s, 0, false};
+           io_dtype == GDR_BF16, s, 0, false, cudaSuccess};
     // in place and in segments: the last segment of a sequence may end before its
     // first one has read the incoming state, which therefore moves aside
     if (initial_state != nullptr && initial_state == final_state && plan.inner > 0) {
@@ -262,8 +269,11 @@ gdr_status_t gdr_linear_prefill(const void *q, const void *k, const void *v, con
         if (pass_state(copy, initial_state, state, s) != cudaSuccess) return GDR_ERR_CUDA;
         initial_state = copy;
     }
-    return status_of(c.scan(q, H_qk, k, H_qk, v, H, d_k, d_v, initial_state, false, final_state, o,
-                            false, false));
+    const ScanArgs p = c.args(q, H_qk, k, H_qk, v, H, initial_state, false, final_state, o, 0, false);
+    c.pass(p, d_k, d_v, false, true, false);
+    c.join(p, d_k, d_v, false);
+    c.pass(p, d_k, d_v, false, false, false);
+    return status_of(c.error);
 }
 
 gdr_status_t gdr_linear_check_workspace(const void *workspace, size_t workspace_bytes, void *stream) {
@@ -338,21 +348,24 @@ gdr_status_t gdr_linear_backward(const void *q, const void *k, const void *v, co
     if (total_T == 0) return status_of(pass_state(d_initial_state, d_final_state, state, s));
 
     Call c{cu_seqlens, decay, num_seqs, total_T, H, plan, lay, static_cast<uint8_t *>(workspace),
-           io_dtype == GDR_BF16, s, 0, false};
-    // heads that share a query/key head: each one's dq and dk in fp32, then their sum
-    const int group = H / H_qk;
+           io_dtype == GDR_BF16, s, 0, false, cudaSuccess};
+    // heads that share a query/key head: each one's dq and dk in fp32, then their sum.
+    // A pass follows one that it does not need, so that neither waits for the other's end.
+    const bool group = H != H_qk;
     float *part = reinterpret_cast<float *>(c.ws + lay.part);
-    cudaError_t r = c.scan(d_o, H, v, H, k, H_qk, d_v, d_k, initial_state, true, nullptr,
-                           group > 1 ? part : dq, group > 1, false);
-    if (r == cudaSuccess && group > 1) r = launch_group_sum(part, total_T, H_qk, group, d_k, c.bf16, dq, s);
-    if (r == cudaSuccess)
-        r = c.scan(v, H, d_o, H, q, H_qk, d_v, d_k, d_final_state, true, nullptr,
-                   group > 1 ? part : dk, group > 1, true);
-    if (r == cudaSuccess && group > 1) r = launch_group_sum(part, total_T, H_qk, group, d_k, c.bf16, dk, s);
-    if (r == cudaSuccess)
-        r = c.scan(k, H_qk, q, H_qk, d_o, H, d_k, d_v, d_final_state, false, d_initial_state, dv,
-                   false, true);
-    return status_of(r);
+    const ScanArgs pq = c.args(d_o, H, v, H, k, H_qk, initial_state, true, nullptr, group ? part : dq, 0, false);
+    const ScanArgs pv = c.args(k, H_qk, q, H_qk, d_o, H, d_final_state, false, d_initial_state, dv, 1, false);
+    const ScanArgs pk = c.args(v, H, d_o, H, q, H_qk, d_final_state, true, nullptr, group ? part : dk, 1, true);
+    c.pass(pq, d_v, d_k, false, true, false);
+    c.pass(pv, d_k, d_v, true, true, false);
+    c.join(pq, d_v, d_k, false);
+    c.join(pv, d_k, d_v, true);
+    c.pass(pq, d_v, d_k, false, false, group);
+    c.sum(part, H_qk, d_k, dq);
+    c.pass(pv, d_k, d_v, true, false, false);
+    c.pass(pk, d_v, d_k, true, false, group);
+    c.sum(part, H_qk, d_k, dk);
+    return status_of(c.error);
 }
 
 }  // extern "C"

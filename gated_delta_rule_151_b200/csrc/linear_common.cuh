@@ -23,7 +23,7 @@
 // runs all segments at once.  A slot is one segment of one sequence, and each
 // sequence has at least one; the states in between are numbered without each
 // sequence's last segment, so there are at most total_T / seg_tokens of them
-// however many sequences there are.
+// however many sequences there are.  dk and dv need the same states, one turned.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -49,7 +49,7 @@ struct ScanArgs {
     int N, total_T, H, HA, HB, HV;
     int seg_tokens;                  // multiple of kScanBlock
     int slots, inner;                // segments, and those that are not their sequence's last
-    int turned;                      // s_in is stored [d_b, d_v]
+    int turned, seg_turned;          // s_in, the states between segments are stored [d_b, d_v]
 };
 
 struct Segment {

@@ -73,25 +73,21 @@ scan_simt_kernel(const ScanArgs p) {
 #pragma unroll
             for (int m = 0; m < M; ++m) f(q, m, q == 0 ? r0 : r1, split + SPL * m);
     };
-    if (used && OUT && seg.index > 0) {
-        const float4 *src = reinterpret_cast<const float4 *>(p.seg + ((size_t)(seg.state - 1) * p.H + h) * (DV * DB));
-        each([&](int q, int m, int r, int c) {
-            const float4 x = src[r * (DB / 4) + c];
-            S[q][2 * m] = make_float2(x.x, x.y);
-            S[q][2 * m + 1] = make_float2(x.z, x.w);
-        });
-    } else if (used && seg.index == 0 && p.s_in != nullptr) {
-        const float *src = p.s_in + state_at;
+    // the state that enters: between segments, the caller's, or zero
+    const float *from = OUT && seg.index > 0 ? p.seg + ((size_t)(seg.state - 1) * p.H + h) * (DV * DB)
+                        : seg.index > 0 || p.s_in == nullptr ? nullptr : p.s_in + state_at;
+    if (used && from != nullptr) {
+        const bool turned = seg.index > 0 ? p.seg_turned : p.turned;
         each([&](int q, int m, int r, int c) {
             float4 x;
-            if (p.turned) x = make_float4(src[(4 * c) * DV + r], src[(4 * c + 1) * DV + r], src[(4 * c + 2) * DV + r], src[(4 * c + 3) * DV + r]);
-            else x = reinterpret_cast<const float4 *>(src)[r * (DB / 4) + c];
+            if (turned) x = make_float4(from[(4 * c) * DV + r], from[(4 * c + 1) * DV + r], from[(4 * c + 2) * DV + r], from[(4 * c + 3) * DV + r]);
+            else x = reinterpret_cast<const float4 *>(from)[r * (DB / 4) + c];
             S[q][2 * m] = make_float2(x.x, x.y);
             S[q][2 * m + 1] = make_float2(x.z, x.w);
         });
     }
 
-    // place u of the scan, and element e (a multiple of 4) of its token's b, v, a
+    // the token at place u of the scan
     auto token = [&](int u) { return (size_t)(seg.t0 + (REV ? seg.len - 1 - u : u)); };
     // what this thread fetches of a tile: where its groups lie in the first one, and how
     // far the next tile's are

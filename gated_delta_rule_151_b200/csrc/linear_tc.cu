@@ -284,24 +284,18 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         float2 S[32];
         if (OUT) wait_for_previous();
-        if (OUT && seg.index > 0) {   // states between segments lie in the order of these threads
-            const float4 *src = reinterpret_cast<const float4 *>(
-                p.seg + ((size_t)(seg.state - 1) * p.H + h) * (D * D)) + t;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float4 x = src[i * kSThreads];
-                S[2 * i] = make_float2(x.x, x.y);
-                S[2 * i + 1] = make_float2(x.z, x.w);
-            }
-        } else if (seg.index > 0 || p.s_in == nullptr) {
+        // the state that enters: between segments, the caller's, or zero
+        const float *from = OUT && seg.index > 0 ? p.seg + ((size_t)(seg.state - 1) * p.H + h) * (D * D)
+                            : seg.index > 0 || p.s_in == nullptr ? nullptr : p.s_in + state_at;
+        if (from == nullptr) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) S[i] = make_float2(0.f, 0.f);
-        } else if (p.turned) {
-            const float *src = p.s_in + state_at + (size_t)half * 64 * D + r;
+        } else if (seg.index > 0 ? p.seg_turned : p.turned) {
+            const float *src = from + (size_t)half * 64 * D + r;
 #pragma unroll
             for (int i = 0; i < 32; ++i) S[i] = make_float2(src[2 * i * D], src[(2 * i + 1) * D]);
         } else {
-            const float4 *src = reinterpret_cast<const float4 *>(p.s_in + state_at + r * D + half * 64);
+            const float4 *src = reinterpret_cast<const float4 *>(from + r * D + half * 64);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float4 x = src[i];
@@ -422,19 +416,12 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             arrive(BAR(kv_free, b % Sh::NB));
             if (OUT && b + 1 < blocks) split_v(b + 1);
         }
-        if (OUT) {
-            if (want_state) {
-                float4 *dst = reinterpret_cast<float4 *>(p.s_out + state_at + r * D + half * 64);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    dst[i] = make_float4(S[2 * i].x, S[2 * i].y, S[2 * i + 1].x, S[2 * i + 1].y);
-            }
-        } else {
-            wait_for_previous();   // an earlier scan of this call may still read the states
-            float4 *dst = reinterpret_cast<float4 *>(seg_out) + t;
+        if (!OUT) wait_for_previous();   // an earlier pass of this call may still read the states
+        if (want_state) {
+            float4 *dst = reinterpret_cast<float4 *>((OUT ? p.s_out + state_at : seg_out) + r * D + half * 64);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                dst[i * kSThreads] = make_float4(S[2 * i].x, S[2 * i].y, S[2 * i + 1].x, S[2 * i + 1].y);
+                dst[i] = make_float4(S[2 * i].x, S[2 * i].y, S[2 * i + 1].x, S[2 * i + 1].y);
         }
     } else if (warp >= 4) {
         // ------------------------------------------ O: 32 channels a warp, all tokens ----
