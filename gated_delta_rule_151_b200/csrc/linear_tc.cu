@@ -66,7 +66,8 @@ struct Misc {
     int abort;
     int scratch[34];
     float pw[kScanBlock + 1];                // x^k
-    alignas(16) float lead[kScanBlock];                  // of S A^T in a full block
+    alignas(16) float lead[kScanBlock];      // of S A^T in a full block
+    alignas(16) float weight[kScanBlock];    // of V in a full block
 };
 
 static_assert(Shape<true>::NS == 3 && Shape<false>::NS == 4, "copies of done and kv_full");
@@ -154,11 +155,11 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) 
         : "r"(taddr));
 }
 
-// The same fragment of 16 lanes by 8 columns of 32 bits to TMEM: registers 2 k and 2 k + 1
+// The same fragment of 16 lanes by 16 columns of 32 bits to TMEM: registers 2 k and 2 k + 1
 // go to column 4 k + lane % 4 of TMEM lanes lane / 4 and lane / 4 + 8.
-__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t *r) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
 
@@ -256,7 +257,10 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
     launch_dependents();
     const float g = clamp_log_gate(p.decay[h]);
     if (tid <= C) m->pw[tid] = expf(g * (float)tid);
-    if (tid < C) m->lead[tid] = expf(g * (float)(REV ? C - 1 - tid : tid + 1));
+    if (tid < C) {
+        m->lead[tid] = expf(g * (float)(REV ? C - 1 - tid : tid + 1));
+        m->weight[tid] = expf(g * (float)(REV ? tid + 1 : C - 1 - tid));
+    }
     if (warp == 0) {
         tmem_alloc(&m->tmem, T_COLS);
         tmem_relinquish();
@@ -306,19 +310,10 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         bool ok = true;
         // (diag(w) V)^T of block b in three bf16 parts to TMEM, the product's other operand:
         // 32 tokens, then the other 32, whose split the first ones' product hides.  A warp
-        // takes 32 channels (its lanes) by 16 of the tokens.  ldmatrix hands a thread tokens
-        // 8 m + 2 (lane % 4) and the next one of channels lane / 4 + {0, 8}, the fragment that
-        // tcgen05.st writes; through shared memory the parts cost 96 KB of its 336 KB of
-        // traffic a block, which was the bound.
-        float2 weight[4];
-        auto weights = [&](int n) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int j = (k >> 1) * 32 + half * 16 + (k & 1) * 8 + 2 * (lane & 3);
-                weight[k] = make_float2(m->pw[REV ? j + 1 : max(n - 1 - j, 0)], m->pw[REV ? j + 2 : max(n - 2 - j, 0)]);
-            }
-        };
-        weights(C);
+        // takes 16 channels (half of its lanes) by the 32 tokens.  ldmatrix hands a thread
+        // tokens 8 m + 2 (lane % 4) and the next one of channels lane / 4 + {0, 8}, the
+        // fragment that tcgen05.st writes; through shared memory the parts cost 96 KB of its
+        // 336 KB of traffic a block, which was the bound.
         auto split_v = [&](int b) {
             const int s = b % Sh::NS, n = block_n(b);
             if (!(ok = warp_wait(BAR(full, s), b / Sh::NS, E_TMA))) return;
@@ -332,49 +327,48 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                     st_shared_v4(stage + Sh::V_OFF + at, 0, 0, 0, 0);
                 }
                 fence_proxy_async();
-                if (!REV) weights(n);
             }
             // (the product that last read this buffer was waited for by its update of S)
             tc_fence_after();
 #pragma unroll
             for (int h2 = 0; h2 < 2; ++h2) {
                 if (b + 1 < blocks || want_state) {
-                    const int j0 = h2 * 32 + half * 16;
+                    const int ch = (warp & 3) * 32 + half * 16 + (lane & 8), j0 = h2 * 32 + 2 * (lane & 3);
                     uint32_t hi[8], mid[8], lo[8];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {      // 16 channels
-                        const int ch = (warp & 3) * 32 + c * 16 + (lane & 8);
-                        const int j = j0 + (lane & 7) + ((lane >> 4) << 3);
+                    for (int k = 0; k < 2; ++k) {      // 16 tokens
+                        const int j = h2 * 32 + k * 16 + (lane & 7) + ((lane >> 4) << 3);
                         const uint32_t at = stage + Sh::V_OFF + (ch >> 6) * 8192 + sw128_offset(j, (ch >> 3) & 7);
                         asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(hi[4 * c]), "=r"(hi[4 * c + 1]), "=r"(hi[4 * c + 2]), "=r"(hi[4 * c + 3])
+                                     : "=r"(hi[4 * k]), "=r"(hi[4 * k + 1]), "=r"(hi[4 * k + 2]), "=r"(hi[4 * k + 3])
                                      : "r"(at)
                                      : "memory");
                     }
+                    float2 weight[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) weight[k] = *reinterpret_cast<const float2 *>(m->weight + j0 + 8 * k);
                     if (n < C) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const int j = j0 + ((e >> 1) & 1) * 8 + 2 * (lane & 3);
+                            const int j = j0 + 8 * (e >> 1);
                             hi[e] = j + 1 < n ? hi[e] : j < n ? hi[e] & 0xffffu : 0u;
+                            if (!REV) weight[e >> 1] = make_float2(m->pw[max(n - 1 - j, 0)], m->pw[max(n - 2 - j, 0)]);
                         }
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float2 minus = make_float2(-1.f, -1.f);
-                        float2 f = __fmul2_rn(make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])), weight[h2 * 2 + ((e >> 1) & 1)]);
+                        float2 f = __fmul2_rn(make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])), weight[e >> 1]);
                         hi[e] = pack_bf16(f.x, f.y);
                         f = __ffma2_rn(make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])), minus, f);
                         mid[e] = pack_bf16(f.x, f.y);
                         f = __ffma2_rn(make_float2(bf16_lo(mid[e]), bf16_hi(mid[e])), minus, f);
                         lo[e] = pack_bf16(f.x, f.y);
                     }
-                    const uint32_t to = tmem + lanes + Sh::T_W + (b % Sh::NB) * 96 + j0 / 2;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        tmem_st_frag(to + (c << 20), hi + 4 * c);
-                        tmem_st_frag(to + (c << 20) + 32, mid + 4 * c);
-                        tmem_st_frag(to + (c << 20) + 64, lo + 4 * c);
-                    }
+                    const uint32_t to = tmem + lanes + ((uint32_t)half << 20) + Sh::T_W + (b % Sh::NB) * 96 + h2 * 16;
+                    tmem_st_frag(to, hi);
+                    tmem_st_frag(to + 32, mid);
+                    tmem_st_frag(to + 64, lo);
                     tmem_wait_st();
                     tc_fence_before();
                 }
