@@ -563,10 +563,16 @@ def gdr_backward(q, k, v, g, beta, initial_state=None, cu_seqlens=None, *, d_o,
 _ACTIVATIONS = {"none": GDR_ACT_NONE, "silu": GDR_ACT_SILU, "sigmoid": GDR_ACT_SIGMOID}
 
 
+# The handle of a device's current stream: 0.2 us by torch's own shortcut, where it
+# has one, against 3 us for a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on(device, stream, run):
     """run(handle of the stream), with ``device`` and ``stream`` current."""
     if stream is None and device.index == torch.cuda.current_device():
-        return run(torch.cuda.current_stream().cuda_stream)
+        return run(_raw_stream(device.index))
     if stream is not None and not isinstance(stream, int) and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.device(device):
