@@ -15,10 +15,13 @@
 // tokens, and S can be its own A operand from TMEM.
 //
 // Rounding.  A, B, V are exact bf16 operands.  P and the copy of S that meets A
-// are rounded to bf16: each adds about one output rounding to o, in
-// quadrature.  The state itself never is: it stays in fp32 registers, and
-// diag(w) V enters its product as three bf16 terms (24 significant bits), so
-// S is as exact as fp32 sums make it over any number of blocks.
+// are rounded to bf16: over many outputs that adds at most about one output
+// rounding to o, in quadrature.  A few outputs of a few tokens may each hang on one
+// score, whose rounding nothing averages out; there (kTwoPartOutputs) P enters
+// its product as two bf16 terms.  The state itself is never rounded: it stays in
+// fp32 registers, and diag(w) V enters its product as three bf16 terms (24
+// significant bits), so S is as exact as fp32 sums make it over any number of
+// blocks.
 //
 // 16 warps: 0-1 turn the scores into P (one row a thread); 2 issues the products
 // of a block's tokens alone (scores, (diag(w) V)^T B), 3 starts the TMA loads into
@@ -46,8 +49,8 @@ struct Shape {
     static constexpr uint32_t STAGE = (OUT ? 3 : 2) * TILE;
     static constexpr uint32_t B_OFF = OUT ? TILE : 0;        // A, B, V in a stage
     static constexpr uint32_t V_OFF = B_OFF + TILE;
-    static constexpr uint32_t P_OFF = NS * STAGE;            // two buffers of 64 x 64 bf16
-    static constexpr uint32_t O_OFF = P_OFF + (OUT ? 2 * 8192 : 0);   // a tile of O on its way out
+    static constexpr uint32_t P_OFF = NS * STAGE;            // two buffers of 64 x 64 bf16, high and low part
+    static constexpr uint32_t O_OFF = P_OFF + (OUT ? 2 * 16384 : 0);  // a tile of O on its way out
     static constexpr uint32_t MISC = O_OFF + (OUT ? TILE : 0);
     // TMEM columns
     static constexpr uint32_t T_KV = 0;                      // NB of 128: (diag(w) V)^T B
@@ -83,6 +86,12 @@ constexpr uint32_t T_COLS = 512;
 constexpr uint32_t ID_N64 = make_idesc(1, 128, 64);
 constexpr uint32_t ID_PV = ID_N64 | kIdescAMN;
 constexpr uint32_t ID_KV = make_idesc(1, 128, 128) | kIdescBMN;
+
+// Up to this many outputs of d_v values P has two parts.  The second one costs the
+// long passes 15 % (1 x 8192 tokens, 16 heads: 61 to 65 us; its gradient 152 to 178),
+// short ones nothing (77 tokens: 17 us either way); one part leaves the result 1.4
+// output roundings off where outputs are many, and up to 2.6 where one score decides.
+constexpr int64_t kTwoPartOutputs = 4096;
 
 enum : uint32_t { E_ALIGN = 1, E_TMA = 2, E_MMA = 4, E_HANDOFF = 8 };
 
@@ -176,7 +185,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-template <bool OUT, bool REV, typename OutT>
+template <bool OUT, bool REV, typename OutT, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
 scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                const __grid_constant__ CUtensorMap mv, const ScanArgs p) {
@@ -428,6 +437,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         float2 lead[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) lead[k] = *reinterpret_cast<const float2 *>(m->lead + 8 * k + 2 * (lane & 3));
+        if (OUT) wait_for_previous();
         for (int b = 0; OUT && b < blocks; ++b) {
             const bool ok = warp_wait(BAR(done, b % 3), b / 3, E_MMA);
             if (group_stop(1, kOThreads, !ok)) break;   // (and the last tile has left)
@@ -519,6 +529,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             __syncwarp();
         };
         if (OUT && blocks > 0) scores(0);
+        if (OUT) wait_for_previous();   // (here and below: the polls that follow do not count that time)
         for (int b = 0; b < blocks && ok; ++b) {
             const int w = b % Sh::NB;
             const bool kv = b + 1 < blocks || want_state;
@@ -549,6 +560,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
     } else if (warp == 3 && OUT) {
         // ------------------------------------------- issuer: S A^T and V^T P^T ----
         for (; issued < min(Sh::NS - 1, blocks); ++issued) load(issued);
+        wait_for_previous();
         for (int b = 0; b < blocks; ++b) {
             // block b - 1 is done, and its state product, which the other issuer committed:
             // its stage takes block b + 2 while S is on its way
@@ -564,7 +576,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             tc_fence_after();
             const uint32_t st = ((b % Sh::NS) * Sh::STAGE) >> 4;
             const uint64_t ad = kmajor + st, vd = mnmajor + (st + (Sh::V_OFF >> 4));
-            const uint64_t pd = kmajor + ((Sh::P_OFF + (b & 1) * 8192) >> 4);
+            const uint64_t pd = kmajor + ((Sh::P_OFF + (b & 1) * 16384) >> 4);
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
@@ -576,8 +588,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_f16_ss(tmem + T_X + (b & 1) * 64, vd + ((k * 2048) >> 4), pd + ((k * 32) >> 4), ID_PV, k != 0);
+                for (int part = TWO; part >= 0; --part)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16_ss(tmem + T_X + (b & 1) * 64, vd + ((k * 2048) >> 4),
+                                   pd + ((part * 8192 + k * 32) >> 4), ID_PV, part != TWO || k != 0);
                 mma_commit(&m->done[b % 3]);
             }
             __syncwarp();
@@ -606,43 +621,51 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             decay[j / 2] = make_float2(a0 >= 0 ? m->pw[max(a0, 0)] : 0.f, a1 >= 0 ? m->pw[max(a1, 0)] : 0.f);
         }
         for (int b = 0; b < blocks; ++b) {
+            if (b == 1) wait_for_previous();
             if (!warp_wait(BAR(sc_full, b & 1), b >> 1, E_MMA)) break;
             if (b >= 2 && !warp_wait(BAR(done, (b - 2) % 3), (b - 2) / 3, E_MMA)) break;
             tc_fence_after();
             const int n = block_n(b);
-            const uint32_t dst = sbase + Sh::P_OFF + (b & 1) * 8192;
+            const uint32_t dst = sbase + Sh::P_OFF + (b & 1) * 16384;
             // 32 columns at a time: they lie on the diagonal of this warp's rows, all on their
             // causal side, or all on the other
             auto columns = [&](auto which) {
                 constexpr int half = decltype(which)::value;
                 const uint32_t at = tmem + lanes + T_X + (b & 1) * 64 + half * 32;
                 uint32_t x[32];
+                auto parts = [&](float2 s, uint32_t &hi, uint32_t &lo) {
+                    hi = pack_bf16(s.x, s.y);
+                    lo = TWO ? pack_bf16(s.x - bf16_lo(hi), s.y - bf16_hi(hi)) : 0;
+                };
+                uint32_t hi[16], lo[16];
                 if (half == warp || (REV && n < C)) {
                     tmem_ld32(at, x);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {    // masked by selection: a score may be anything there
                         const int j = half * 32 + e;
-                        const float2 s = __fmul2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), decay[j / 2]);
-                        x[e / 2] = pack_bf16((REV ? j >= i && j < n : j <= i) ? s.x : 0.f,
-                                             (REV ? j + 1 >= i && j + 1 < n : j + 1 <= i) ? s.y : 0.f);
+                        float2 s = __fmul2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), decay[j / 2]);
+                        s.x = (REV ? j >= i && j < n : j <= i) ? s.x : 0.f;
+                        s.y = (REV ? j + 1 >= i && j + 1 < n : j + 1 <= i) ? s.y : 0.f;
+                        parts(s, hi[e / 2], lo[e / 2]);
                     }
                 } else if (REV ? half < warp : half > warp) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = 0;
+                    for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0;
                 } else {
                     tmem_ld32(at, x);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 s = __fmul2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
-                                                    decay[(half * 32 + e) / 2]);
-                        x[e / 2] = pack_bf16(s.x, s.y);
-                    }
+                    for (int e = 0; e < 32; e += 2)
+                        parts(__fmul2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), decay[(half * 32 + e) / 2]),
+                              hi[e / 2], lo[e / 2]);
                 }
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    st_shared_v4(dst + sw128_offset(i, half * 4 + q), x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t to = dst + sw128_offset(i, half * 4 + q);
+                    st_shared_v4(to, hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+                    if (TWO) st_shared_v4(to + 8192, lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+                }
             };
             columns(std::integral_constant<int, 0>{});
             columns(std::integral_constant<int, 1>{});
@@ -674,14 +697,21 @@ bool make_tile_map(CUtensorMap *map, const void *base, int total_T, int H) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool OUT, bool REV, typename OutT>
+template <bool OUT, bool REV, typename OutT, bool TWO>
 cudaError_t launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mv,
                    const ScanArgs &p, bool after, cudaStream_t stream) {
-    auto fn = scan_tc_kernel<OUT, REV, OutT>;
+    auto fn = scan_tc_kernel<OUT, REV, OutT, TWO>;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(fn), smem_bytes<OUT>());
     if (e != cudaSuccess) return e;
     return launch_kernel(after, fn, dim3((unsigned)(OUT ? p.slots : p.inner) * p.H), kThreads, smem_bytes<OUT>(),
                          stream, ma, mb, mv, p);
+}
+
+template <bool REV, typename OutT>
+cudaError_t launch_out(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mv,
+                       const ScanArgs &p, bool after, cudaStream_t stream) {
+    return (int64_t)p.total_T * p.H <= kTwoPartOutputs ? launch<true, REV, OutT, true>(ma, mb, mv, p, after, stream)
+                                                       : launch<true, REV, OutT, false>(ma, mb, mv, p, after, stream);
 }
 
 }  // namespace
@@ -693,13 +723,13 @@ cudaError_t launch_scan_tc(const ScanArgs &p, bool reverse, bool states, bool ou
         !make_tile_map(&mv, p.v, p.total_T, p.HV))
         return cudaErrorInvalidValue;
     if (states)
-        return reverse ? launch<false, true, __nv_bfloat16>(ma, mb, mv, p, after, stream)
-                       : launch<false, false, __nv_bfloat16>(ma, mb, mv, p, after, stream);
+        return reverse ? launch<false, true, float, false>(ma, mb, mv, p, after, stream)
+                       : launch<false, false, float, false>(ma, mb, mv, p, after, stream);
     if (out_f32)
-        return reverse ? launch<true, true, float>(ma, mb, mv, p, after, stream)
-                       : launch<true, false, float>(ma, mb, mv, p, after, stream);
-    return reverse ? launch<true, true, __nv_bfloat16>(ma, mb, mv, p, after, stream)
-                   : launch<true, false, __nv_bfloat16>(ma, mb, mv, p, after, stream);
+        return reverse ? launch_out<true, float>(ma, mb, mv, p, after, stream)
+                       : launch_out<false, float>(ma, mb, mv, p, after, stream);
+    return reverse ? launch_out<true, __nv_bfloat16>(ma, mb, mv, p, after, stream)
+                   : launch_out<false, __nv_bfloat16>(ma, mb, mv, p, after, stream);
 }
 
 }  // namespace gdr
