@@ -278,7 +278,7 @@ cudaError_t launch_dims(const ScanArgs &p, int d_b, int d_v, bool reverse, bool 
 // ------------------------------------------------ states between segments ----
 
 // X_0 = the first segment's state, X_s = x^{tokens of s} X_{s-1} + (state of s):
-// every block takes 1024 elements along one sequence's segments.  All of them
+// every block takes some of the elements along one sequence's segments.  All of them
 // but the first in scan order are full (the last one's state is not needed).
 constexpr int kJoinThreads = 256;
 
@@ -293,24 +293,24 @@ scan_join_kernel(const ScanArgs p, int elements, bool reverse) {
     if (p.cu == nullptr) slot *= p.inner / p.N;
     const Segment seg = find_segment(p, slot, true, reverse, scratch, kJoinThreads);
     if (seg.n < 0 || seg.index != 0 || seg.count < 3) return;
-    const int e = (blockIdx.y * kJoinThreads + threadIdx.x) * 4;
-    if (e >= elements) return;
     const float w = expf(clamp_log_gate(p.decay[h]) * (float)p.seg_tokens);
     const size_t step = (size_t)p.H * elements / 4;
-    float4 *at = reinterpret_cast<float4 *>(p.seg + ((size_t)seg.state * p.H + h) * elements + e);
     const int end = min(seg.count - 1, p.inner - seg.state);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < end; s += 8) {   // eight loads in flight
-        float4 y[8];
+    for (int e = (blockIdx.y * kJoinThreads + threadIdx.x) * 4; e < elements; e += gridDim.y * kJoinThreads * 4) {
+        float4 *at = reinterpret_cast<float4 *>(p.seg + ((size_t)seg.state * p.H + h) * elements + e);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < end; s += 8) {   // eight loads in flight
+            float4 y[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (s + u < end) y[u] = at[(size_t)(s + u) * step];
+            for (int u = 0; u < 8; ++u)
+                if (s + u < end) y[u] = at[(size_t)(s + u) * step];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (s + u >= end) break;
-            x = make_float4(fmaf(w, x.x, y[u].x), fmaf(w, x.y, y[u].y), fmaf(w, x.z, y[u].z),
-                            fmaf(w, x.w, y[u].w));
-            if (s + u > 0) at[(size_t)(s + u) * step] = x;
+            for (int u = 0; u < 8; ++u) {
+                if (s + u >= end) break;
+                x = make_float4(fmaf(w, x.x, y[u].x), fmaf(w, x.y, y[u].y), fmaf(w, x.z, y[u].z),
+                                fmaf(w, x.w, y[u].w));
+                if (s + u > 0) at[(size_t)(s + u) * step] = x;
+            }
         }
     }
 }
@@ -437,7 +437,9 @@ cudaError_t launch_scan_simt(const ScanArgs &p, int d_b, int d_v, bool reverse, 
 }
 
 cudaError_t launch_scan_join(const ScanArgs &p, int elements, bool reverse, cudaStream_t stream) {
-    const dim3 grid((unsigned)(p.cu == nullptr ? p.N : p.inner) * p.H, (elements / 4 + kJoinThreads - 1) / kJoinThreads);
+    // packed lengths: most blocks only find that they have nothing to do, so there are fewer
+    const int all = (elements / 4 + kJoinThreads - 1) / kJoinThreads;
+    const dim3 grid((unsigned)(p.cu == nullptr ? p.N : p.inner) * p.H, p.cu == nullptr ? all : std::min(all, 4));
     return launch_kernel(true, scan_join_kernel, grid, kJoinThreads, 0, stream, p, elements, reverse);
 }
 
