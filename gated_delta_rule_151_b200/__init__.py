@@ -2,7 +2,8 @@
 
 ``gdr`` is the ctypes binding of libgdr.so (include/gdr.h): chunked prefill
 and single-token decode in scalar-gate (Gated DeltaNet) and channel-gate
-(Kimi Delta Attention) modes.  ``inputs`` draws the seeded synthetic
+(Kimi Delta Attention) modes, linear attention with a decay for each head and
+the gated norms around a block.  ``inputs`` draws the seeded synthetic
 workloads.  Importing the package loads nothing; the library is loaded on the
 first call and every call raises if it is missing.
 """

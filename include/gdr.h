@@ -467,8 +467,8 @@ GDR_API gdr_status_t gdr_backward(const void *q, const void *k, const void *v, c
  * run in a fixed order: the same inputs give the same bits.
  *
  * bf16 with d_k = d_v = 128 runs on the tensor cores: 64-token blocks, the
- * score block and the copy of the state that meets the queries rounded to
- * bf16, the state itself fp32 throughout.  Other shapes and fp32 run in fp32
+ * copy of the state that meets the queries and (with more than 4096 outputs of
+ * d_v values) the scores rounded to bf16, the state itself fp32 throughout.  Other shapes and fp32 run in fp32
  * on the CUDA cores.  Infinities and NaN stay inside their (sequence, head);
  * a non-finite value in v or k leaves NaN in every later output it reaches.
  *
