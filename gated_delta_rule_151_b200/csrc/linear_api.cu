@@ -187,7 +187,7 @@ struct Call {
         error = launch_scan_join(p, d_b * d_v, reverse, stream);
     }
     void sum(const float *part, int H_qk, int d, void *out) {
-        if (error == cudaSuccess && H != H_qk) error = launch_group_sum(part, total_T, H_qk, H / H_qk, d, bf16, out, stream);
+        if (error == cudaSuccess && H != H_qk) error = launch_group_sum(part, cu, N, total_T, H_qk, H / H_qk, d, bf16, out, stream);
     }
 };
 

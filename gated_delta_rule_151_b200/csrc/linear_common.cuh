@@ -142,8 +142,8 @@ cudaError_t launch_scan_simt(const ScanArgs &p, int d_b, int d_v, bool reverse, 
 // Segments' own states -> states behind each segment, in place (after the states' pass).
 cudaError_t launch_scan_join(const ScanArgs &p, int elements, bool reverse, cudaStream_t stream);
 // [T, H, d] fp32 partial gradients summed over each group of H / H_qk heads (after a pass).
-cudaError_t launch_group_sum(const float *part, int64_t T, int H_qk, int group, int d, bool bf16,
-                             void *out, cudaStream_t stream);
+cudaError_t launch_group_sum(const float *part, const int32_t *cu, int N, int64_t T, int H_qk, int group, int d,
+                             bool bf16, void *out, cudaStream_t stream);
 cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, const float *decay,
                                  float *state, int N, int Hqk, int H, int DK, int DV, bool bf16,
                                  void *o, cudaStream_t stream);

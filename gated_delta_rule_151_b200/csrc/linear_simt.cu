@@ -319,12 +319,19 @@ scan_join_kernel(const ScanArgs p, int elements, bool reverse) {
 
 constexpr int kSumThreads = 256;
 
+// (Tokens behind the last packed sequence have no parts: they stay as they are.)
 template <typename Out>
 __global__ void __launch_bounds__(kSumThreads)
-group_sum_kernel(const float *__restrict__ part, int64_t vecs, int group, int d4, Out *__restrict__ out) {
+group_sum_kernel(const float *__restrict__ part, const int32_t *__restrict__ cu, int N, int64_t T, int H_qk,
+                 int group, int d4, Out *__restrict__ out) {
     launch_dependents();
     wait_for_previous();
-    for (int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x; i < vecs;
+    int64_t first = 0, end = T * H_qk * d4;
+    if (cu != nullptr) {
+        first = min(max((int64_t)cu[0], (int64_t)0), T) * H_qk * d4;
+        end = min(max((int64_t)cu[N], (int64_t)0), T) * H_qk * d4;
+    }
+    for (int64_t i = first + (int64_t)blockIdx.x * kSumThreads + threadIdx.x; i < end;
          i += (int64_t)gridDim.x * kSumThreads) {
         const int64_t head = i / d4;
         const float4 *src = reinterpret_cast<const float4 *>(part) + head * group * d4 + i % d4;
@@ -443,14 +450,14 @@ cudaError_t launch_scan_join(const ScanArgs &p, int elements, bool reverse, cuda
     return launch_kernel(true, scan_join_kernel, grid, kJoinThreads, 0, stream, p, elements, reverse);
 }
 
-cudaError_t launch_group_sum(const float *part, int64_t T, int H_qk, int group, int d, bool bf16,
-                             void *out, cudaStream_t stream) {
-    const int64_t vecs = T * H_qk * (d / 4);
-    const unsigned grid = (unsigned)std::min<int64_t>((vecs + kSumThreads - 1) / kSumThreads, 148 * 16);
+cudaError_t launch_group_sum(const float *part, const int32_t *cu, int N, int64_t T, int H_qk, int group, int d,
+                             bool bf16, void *out, cudaStream_t stream) {
+    const int64_t groups = (T * H_qk * (d / 4) + kSumThreads - 1) / kSumThreads;
+    const dim3 grid((unsigned)std::min<int64_t>(groups, 148 * 16));
     if (bf16)
-        return launch_kernel(true, group_sum_kernel<__nv_bfloat16>, dim3(grid), kSumThreads, 0, stream, part, vecs,
+        return launch_kernel(true, group_sum_kernel<__nv_bfloat16>, grid, kSumThreads, 0, stream, part, cu, N, T, H_qk,
                              group, d / 4, static_cast<__nv_bfloat16 *>(out));
-    return launch_kernel(true, group_sum_kernel<float>, dim3(grid), kSumThreads, 0, stream, part, vecs, group, d / 4,
+    return launch_kernel(true, group_sum_kernel<float>, grid, kSumThreads, 0, stream, part, cu, N, T, H_qk, group, d / 4,
                          static_cast<float *>(out));
 }
 

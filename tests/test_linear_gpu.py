@@ -235,6 +235,7 @@ def test_streams_and_graph():
     torch.cuda.synchronize()
     got_x, got_y = run(x, stream=s1), run(y, stream=s2.cuda_stream)
     torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(run(x, stream=0), want_x))     # the legacy stream's handle
     assert all(torch.equal(a, b) for a, b in zip(got_x + got_y, want_x + want_y))
     graph = torch.cuda.CUDAGraph()
     held = {n: t.clone() for n, t in x.items() if t is not None}
@@ -245,6 +246,40 @@ def test_streams_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out + grads, want_y + want_b))
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.float32, 16), (torch.bfloat16, 128)], ids=["f32", "bf16"])
+def test_rows_behind_the_last_sequence_stay(dtype, d):
+    """A batch padded behind its last sequence: what lies there is neither read into a result nor written."""
+    T, end, Hqk, H = 200, 131, 2, 4
+    _, x = make(T, Hqk, H, d, d, dtype, 2, [0, 60, end], True, seed=14)
+    short = {n: (t[:end].contiguous() if n in ("q", "k", "v", "d_o") else t) for n, t in x.items()}
+    want = gdr.gdr_linear_prefill(short["q"], short["k"], short["v"], short["decay"], short["state"], short["cu"])
+    want_g = gdr.gdr_linear_backward(short["q"], short["k"], short["v"], short["decay"], short["state"], short["cu"],
+                                     d_o=short["d_o"], d_final_state=short["d_final"])
+    for n in ("q", "k", "v", "d_o"):
+        x[n][end:] = float("nan")
+    o = torch.full((T, H, d), 7.0, dtype=dtype, device="cuda")
+    _, fin = gdr.gdr_linear_prefill(x["q"], x["k"], x["v"], x["decay"], x["state"], x["cu"], o=o)
+    assert (o[end:] == 7.0).all()
+    tol = 2.0 ** -7 if dtype == torch.bfloat16 else 1e-5     # (the lengths are cut elsewhere: another order of sums)
+    assert (o[:end].double() - want[0].double()).norm() <= tol * want[0].double().norm()
+    assert (fin - want[1]).double().norm() <= 1e-5 * want[1].double().norm()
+    # the gradients' tensors come from the binding: what lies behind is whatever the memory held
+    lib = gdr.load_library()
+    dq, dk, dv = (torch.full_like(t, 7.0) for t in (x["q"], x["k"], x["v"]))
+    dS = torch.empty_like(x["state"])
+    need = gdr.gdr_linear_workspace_size(2, T, Hqk, H, d, d, gdr._io_code(dtype), True)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")       # NaN wherever it is read unwritten
+    status = lib.gdr_linear_backward(
+        x["q"].data_ptr(), x["k"].data_ptr(), x["v"].data_ptr(), x["decay"].data_ptr(), x["state"].data_ptr(),
+        x["cu"].data_ptr(), 2, T, Hqk, H, d, d, gdr._io_code(dtype), x["d_o"].data_ptr(), x["d_final"].data_ptr(),
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dS.data_ptr(), ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+    assert status == gdr.GDR_OK
+    for g, w in zip((dq, dk, dv), want_g):
+        assert (g[end:] == 7.0).all()
+        assert (g[:end].double() - w.double()).norm() <= tol * w.double().norm()
+    assert (dS - want_g[3]).double().norm() <= 1e-5 * want_g[3].double().norm()
 
 
 def test_malformed_cu_seqlens_stays_in_bounds():

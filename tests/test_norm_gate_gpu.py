@@ -103,6 +103,27 @@ def test_backward_sizes(rows, dim, dtype):
         assert torch.equal(r, a), k
 
 
+@pytest.mark.parametrize("act", ["none", "silu", "sigmoid"])
+def test_gradient_against_differences(act):
+    """Along random directions of every input, against central differences of the 64-bit definition."""
+    c = make(13, 72, torch.float32, FULL + ("dy", "dn"), seed=5)
+    d = gpu(c)
+    got = gdr.gdr_norm_gate_backward(d["x"], d["dy"], d["dn"], *(d[k] for k in FULL), scale=0.5, eps=EPS, activation=act)
+    g = torch.Generator().manual_seed(6)
+
+    def loss(**over):
+        a = {k: over.get(k, c[k].double()) for k in ("x",) + FULL}
+        y, n = ref.norm_gate(*a.values(), 0.5, EPS, act)
+        return float((y * c["dy"].double()).sum() + (n * c["dn"].double()).sum())
+
+    for k, r in zip(("x",) + FULL, got):
+        way, h = torch.randn(c[k].shape, generator=g).double(), 1e-4
+        diff = (loss(**{k: c[k].double() + h * way}) - loss(**{k: c[k].double() - h * way})) / (2 * h)
+        along = (r.double().cpu() * way)
+        # the difference's own error is h^2 times a third derivative of order one; fp32 gradients 1e-5
+        assert abs(float(along.sum()) - diff) <= 1e-5 * float(along.abs().sum()), k
+
+
 def test_extreme_rows():
     """A row of zeros, huge and tiny rows, and gates far out: finite, and as the definition."""
     x = torch.zeros(6, 128)
