@@ -603,12 +603,13 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _scratch(workspace, need, device):
-    """(pointer, bytes) of the caller's workspace or of a new one, and what keeps it alive."""
+def _scratch(workspace, need, like, device):
+    """(pointer, bytes) of the caller's workspace or of a new one, and what keeps it alive.
+    ``like``: an fp32 tensor of the call (its new_empty takes half of torch.empty's time)."""
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = like.new_empty((need + 3) // 4)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -617,11 +618,12 @@ def _scratch(workspace, need, device):
 def _linear_args(q, k, v, decay, cu_seqlens, num_seqs):
     """Checks what the linear-attention calls share; returns their sizes."""
     _need(q, "q", ndim=3)
-    _need(v, "v", q.dtype, 3)
-    T, Hqk, dk = q.shape
-    H, dv = v.shape[1], v.shape[2]
-    dev, io = q.device, q.dtype
-    _given(k, "k", q.shape, io, dev)
+    shape, dev, io = q.shape, q.device, q.dtype
+    T, Hqk, dk = shape
+    _given(k, "k", shape, io, dev)
+    if v is None or v.dim() != 3:
+        raise ValueError("v must be [T, H, d_v]")
+    _, H, dv = v.shape
     _given(v, "v", (T, H, dv), io, dev)
     _given(decay, "decay", (H,), torch.float32, dev)
     if cu_seqlens is not None:
@@ -675,8 +677,8 @@ def gdr_linear_prefill(q, k, v, decay, initial_state=None, cu_seqlens=None, *, n
         out = torch.empty_like(v) if o is None else o
         fin = final_state
         if fin is None and output_final_state:
-            fin = torch.empty(state, dtype=torch.float32, device=dev)
-        ws, ws_bytes, _keep = _scratch(workspace, need, dev)
+            fin = decay.new_empty(state)
+        ws, ws_bytes, _keep = _scratch(workspace, need, decay, dev)
         st = load_library().gdr_linear_prefill(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), _at(initial_state),
             _at(cu_seqlens), N, T, Hqk, H, dk, dv, code, out.data_ptr(), _at(fin), ws, ws_bytes,
@@ -741,9 +743,8 @@ def gdr_linear_backward(q, k, v, decay, initial_state=None, cu_seqlens=None, *, 
 
     def run(stream_ptr):
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        dh0 = (torch.empty(state, dtype=torch.float32, device=dev)
-               if want_d_initial_state else None)
-        ws, ws_bytes, _keep = _scratch(workspace, need, dev)
+        dh0 = decay.new_empty(state) if want_d_initial_state else None
+        ws, ws_bytes, _keep = _scratch(workspace, need, decay, dev)
         st = load_library().gdr_linear_backward(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), _at(initial_state),
             _at(cu_seqlens), N, T, Hqk, H, dk, dv, code, d_o.data_ptr(), _at(d_final_state),
@@ -845,7 +846,7 @@ def gdr_norm_gate_backward(x, dy=None, dn=None, weight=None, gate=None, residual
         new = lambda like: None if like is None else torch.empty_like(like)  # noqa: E731
         dx, dweight, dgate, dres = new(x), new(weight), new(gate), new(residual)
         dnext = new(next_weight) if dn is not None else None
-        ws, ws_bytes, _keep = _scratch(workspace, need, dev)
+        ws, ws_bytes, _keep = _scratch(workspace, need, weight if weight is not None else next_weight, dev)
         st = load_library().gdr_norm_gate_backward(
             x.data_ptr(), _at(weight), _at(gate), _at(residual), _at(next_weight), rows, dim,
             float(scale), float(eps), act, code, _at(dy), _at(dn), dx.data_ptr(), _at(dweight),
