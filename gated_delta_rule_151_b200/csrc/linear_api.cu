@@ -103,7 +103,7 @@ Plan make_plan(int N, int total_T, int H, int d_k, int d_v, bool bf16, bool equa
 // incoming state, the states between segments (forward scan, reverse scan), fp32
 // partial gradients.
 struct Layout {
-    size_t status, copy, seg[2], part, total;
+    size_t status, copy, seg[2], part[2], total;
     uint32_t words;
 };
 
@@ -116,8 +116,10 @@ Layout make_layout(const Plan &p, int N, int total_T, int H_qk, int H, int d_k, 
     l.copy = l.status + up256((size_t)l.words * 4);
     l.seg[0] = l.copy + (p.inner > 0 && !backward ? up256(N * state) : 0);
     l.seg[1] = l.seg[0] + up256(p.inner * state);
-    l.part = l.seg[1] + (backward ? up256(p.inner * state) : 0);
-    l.total = l.part + (backward && H != H_qk ? up256((size_t)total_T * H * d_k * 4) : 0);
+    const size_t part = backward && H != H_qk ? up256((size_t)total_T * H * d_k * 4) : 0;
+    l.part[0] = l.seg[1] + (backward ? up256(p.inner * state) : 0);
+    l.part[1] = l.part[0] + part;
+    l.total = l.part[1] + part;
     return l;
 }
 
@@ -167,15 +169,17 @@ struct Call {
         p.inner = plan.inner;
         p.turned = turned;
         p.seg_turned = seg_turned;
+        p.late = 0;
         return p;
     }
 
     // One pass, and the pass between segments; nothing after an error.
-    void pass(ScanArgs p, int d_b, int d_v, bool reverse, bool states, bool out_f32) {
+    void pass(ScanArgs p, int d_b, int d_v, bool reverse, bool states, bool out_f32, bool late = false) {
         if (error != cudaSuccess || (states && plan.inner == 0)) return;
         const bool tc = tensor_cores(d_b, d_v, bf16);
         p.status = reinterpret_cast<uint32_t *>(ws + lay.status) + used;
         p.status_words = tc ? lay.words : 0;
+        p.late = late;
         used += (uint32_t)(states ? plan.inner : plan.slots) * H;
         error = tc ? launch_scan_tc(p, reverse, states, out_f32, launched, stream)
                    : launch_scan_simt(p, d_b, d_v, reverse, states, bf16, out_f32, launched, stream);
@@ -185,9 +189,6 @@ struct Call {
         // (of two segments the first one's own state is what the second starts from)
         if (error != cudaSuccess || plan.inner == 0 || (cu == nullptr && plan.inner == N)) return;
         error = launch_scan_join(p, d_b * d_v, reverse, stream);
-    }
-    void sum(const float *part, int H_qk, int d, void *out) {
-        if (error == cudaSuccess && H != H_qk) error = launch_group_sum(part, cu, N, total_T, H_qk, H / H_qk, d, bf16, out, stream);
     }
 };
 
@@ -349,22 +350,26 @@ gdr_status_t gdr_linear_backward(const void *q, const void *k, const void *v, co
 
     Call c{cu_seqlens, decay, num_seqs, total_T, H, plan, lay, static_cast<uint8_t *>(workspace),
            io_dtype == GDR_BF16, s, 0, false, cudaSuccess};
-    // heads that share a query/key head: each one's dq and dk in fp32, then their sum.
-    // A pass follows one that it does not need, so that neither waits for the other's end.
+    // heads that share a query/key head: each one's dq and dk in fp32, then their sums.
+    // A pass follows one that it does not need, so that neither waits for the other's
+    // end; the first output pass waits for all states, and vouches for them.
     const bool group = H != H_qk;
-    float *part = reinterpret_cast<float *>(c.ws + lay.part);
-    const ScanArgs pq = c.args(d_o, H, v, H, k, H_qk, initial_state, true, nullptr, group ? part : dq, 0, false);
+    float *part[2] = {reinterpret_cast<float *>(c.ws + lay.part[0]), reinterpret_cast<float *>(c.ws + lay.part[1])};
+    const ScanArgs pq = c.args(d_o, H, v, H, k, H_qk, initial_state, true, nullptr, group ? part[0] : dq, 0, false);
     const ScanArgs pv = c.args(k, H_qk, q, H_qk, d_o, H, d_final_state, false, d_initial_state, dv, 1, false);
-    const ScanArgs pk = c.args(v, H, d_o, H, q, H_qk, d_final_state, true, nullptr, group ? part : dk, 1, true);
+    const ScanArgs pk = c.args(v, H, d_o, H, q, H_qk, d_final_state, true, nullptr, group ? part[1] : dk, 1, true);
     c.pass(pq, d_v, d_k, false, true, false);
     c.pass(pv, d_k, d_v, true, true, false);
     c.join(pq, d_v, d_k, false);
     c.join(pv, d_k, d_v, true);
     c.pass(pq, d_v, d_k, false, false, group);
-    c.sum(part, H_qk, d_k, dq);
-    c.pass(pv, d_k, d_v, true, false, false);
-    c.pass(pk, d_v, d_k, true, false, group);
-    c.sum(part, H_qk, d_k, dk);
+    c.pass(pv, d_k, d_v, true, false, false, true);
+    c.pass(pk, d_v, d_k, true, false, group, true);
+    if (c.error == cudaSuccess && group) {
+        const float *const parts[2] = {part[0], part[1]};
+        void *const sums[2] = {dq, dk};
+        c.error = launch_group_sum(parts, cu_seqlens, num_seqs, total_T, H_qk, H / H_qk, d_k, c.bf16, sums, s);
+    }
     return status_of(c.error);
 }
 

@@ -50,6 +50,7 @@ struct ScanArgs {
     int seg_tokens;                  // multiple of kScanBlock
     int slots, inner;                // segments, and those that are not their sequence's last
     int turned, seg_turned;          // s_in, the states between segments are stored [d_b, d_v]
+    int late;                        // output pass behind another one whose results it does not need
 };
 
 struct Segment {
@@ -141,9 +142,9 @@ cudaError_t launch_scan_simt(const ScanArgs &p, int d_b, int d_v, bool reverse, 
                              bool bf16, bool out_f32, bool after, cudaStream_t stream);
 // Segments' own states -> states behind each segment, in place (after the states' pass).
 cudaError_t launch_scan_join(const ScanArgs &p, int elements, bool reverse, cudaStream_t stream);
-// [T, H, d] fp32 partial gradients summed over each group of H / H_qk heads (after a pass).
-cudaError_t launch_group_sum(const float *part, const int32_t *cu, int N, int64_t T, int H_qk, int group, int d,
-                             bool bf16, void *out, cudaStream_t stream);
+// [T, H, d] fp32 partial gradients (dq's and dk's) summed over each group of H / H_qk heads (after a pass).
+cudaError_t launch_group_sum(const float *const (&part)[2], const int32_t *cu, int N, int64_t T, int H_qk,
+                             int group, int d, bool bf16, void *const (&out)[2], cudaStream_t stream);
 cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, const float *decay,
                                  float *state, int N, int Hqk, int H, int DK, int DV, bool bf16,
                                  void *o, cudaStream_t stream);

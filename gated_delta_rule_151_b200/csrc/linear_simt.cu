@@ -51,8 +51,9 @@ scan_simt_kernel(const ScanArgs p) {
     __shared__ int scratch[34];
     const int tid = threadIdx.x;
     const int slot = blockIdx.x / p.H, h = blockIdx.x % p.H;
-    launch_dependents();
-    wait_for_previous();
+    if (!OUT) launch_dependents();
+    if (!OUT || !p.late) wait_for_previous();
+    if (OUT) launch_dependents();     // (an output pass behind this one goes by what this one waited for)
     if (OUT && blockIdx.x == 0 && tid == 0) *p.header = p.status_words;
     const Segment seg = find_segment(p, slot, !OUT, REV, scratch, NT);
     if (seg.n < 0) return;
@@ -231,6 +232,7 @@ scan_simt_kernel(const ScanArgs p) {
         }
         buf = after;
     }
+    if (OUT && p.late) wait_for_previous();
     float *out_state = OUT ? (last ? p.s_out : nullptr) : p.seg;
     if (used && out_state != nullptr) {
         float4 *dst = reinterpret_cast<float4 *>(out_state + (OUT ? state_at : ((size_t)seg.state * p.H + h) * (DV * DB)));
@@ -322,9 +324,10 @@ constexpr int kSumThreads = 256;
 // (Tokens behind the last packed sequence have no parts: they stay as they are.)
 template <typename Out>
 __global__ void __launch_bounds__(kSumThreads)
-group_sum_kernel(const float *__restrict__ part, const int32_t *__restrict__ cu, int N, int64_t T, int H_qk,
-                 int group, int d4, Out *__restrict__ out) {
-    launch_dependents();
+group_sum_kernel(const float *__restrict__ part0, const float *__restrict__ part1, const int32_t *__restrict__ cu,
+                 int N, int64_t T, int H_qk, int group, int d4, Out *__restrict__ out0, Out *__restrict__ out1) {
+    const float *part = blockIdx.y == 0 ? part0 : part1;
+    Out *out = blockIdx.y == 0 ? out0 : out1;
     wait_for_previous();
     int64_t first = 0, end = T * H_qk * d4;
     if (cu != nullptr) {
@@ -450,15 +453,16 @@ cudaError_t launch_scan_join(const ScanArgs &p, int elements, bool reverse, cuda
     return launch_kernel(true, scan_join_kernel, grid, kJoinThreads, 0, stream, p, elements, reverse);
 }
 
-cudaError_t launch_group_sum(const float *part, const int32_t *cu, int N, int64_t T, int H_qk, int group, int d,
-                             bool bf16, void *out, cudaStream_t stream) {
+cudaError_t launch_group_sum(const float *const (&part)[2], const int32_t *cu, int N, int64_t T, int H_qk,
+                             int group, int d, bool bf16, void *const (&out)[2], cudaStream_t stream) {
     const int64_t groups = (T * H_qk * (d / 4) + kSumThreads - 1) / kSumThreads;
-    const dim3 grid((unsigned)std::min<int64_t>(groups, 148 * 16));
+    const dim3 grid((unsigned)std::min<int64_t>(groups, 148 * 8), 2);
     if (bf16)
-        return launch_kernel(true, group_sum_kernel<__nv_bfloat16>, grid, kSumThreads, 0, stream, part, cu, N, T, H_qk,
-                             group, d / 4, static_cast<__nv_bfloat16 *>(out));
-    return launch_kernel(true, group_sum_kernel<float>, grid, kSumThreads, 0, stream, part, cu, N, T, H_qk, group, d / 4,
-                         static_cast<float *>(out));
+        return launch_kernel(true, group_sum_kernel<__nv_bfloat16>, grid, kSumThreads, 0, stream, part[0], part[1], cu, N,
+                             T, H_qk, group, d / 4, static_cast<__nv_bfloat16 *>(out[0]),
+                             static_cast<__nv_bfloat16 *>(out[1]));
+    return launch_kernel(true, group_sum_kernel<float>, grid, kSumThreads, 0, stream, part[0], part[1], cu, N, T, H_qk,
+                         group, d / 4, static_cast<float *>(out[0]), static_cast<float *>(out[1]));
 }
 
 cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, const float *decay,

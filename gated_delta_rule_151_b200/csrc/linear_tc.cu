@@ -263,7 +263,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         __syncwarp();
         if (blocks > 0) load(issued++);
     }
-    launch_dependents();
+    // (an output pass behind this one goes by what this one waits for)
+    if (!OUT || p.late) launch_dependents();
+    auto wait_here = [&]() {
+        if (OUT && !p.late) wait_for_previous();
+    };
     const float g = clamp_log_gate(p.decay[h]);
     if (tid <= C) m->pw[tid] = expf(g * (float)tid);
     if (tid < C) {
@@ -296,7 +300,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         const int r = (warp & 3) * 32 + lane, half = (warp - 8) >> 2;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         float2 S[32];
-        if (OUT) wait_for_previous();
+        wait_here();
+        if (OUT && !p.late) launch_dependents();
         // the state that enters: between segments, the caller's, or zero
         const float *from = OUT && seg.index > 0 ? p.seg + ((size_t)(seg.state - 1) * p.H + h) * (D * D)
                             : seg.index > 0 || p.s_in == nullptr ? nullptr : p.s_in + state_at;
@@ -419,7 +424,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             arrive(BAR(kv_free, b % Sh::NB));
             if (OUT && b + 1 < blocks) split_v(b + 1);
         }
-        if (!OUT) wait_for_previous();   // an earlier pass of this call may still read the states
+        // an earlier pass of this call may still read the states, or run beside this one
+        if (!OUT || p.late) wait_for_previous();
         if (want_state) {
             float4 *dst = reinterpret_cast<float4 *>((OUT ? p.s_out + state_at : seg_out) + r * D + half * 64);
 #pragma unroll
@@ -437,7 +443,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         float2 lead[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) lead[k] = *reinterpret_cast<const float2 *>(m->lead + 8 * k + 2 * (lane & 3));
-        if (OUT) wait_for_previous();
+        wait_here();
         for (int b = 0; OUT && b < blocks; ++b) {
             const bool ok = warp_wait(BAR(done, b % 3), b / 3, E_MMA);
             if (group_stop(1, kOThreads, !ok)) break;   // (and the last tile has left)
@@ -529,7 +535,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             __syncwarp();
         };
         if (OUT && blocks > 0) scores(0);
-        if (OUT) wait_for_previous();   // (here and below: the polls that follow do not count that time)
+        wait_here();   // (here and below: the polls that follow do not count that time)
         for (int b = 0; b < blocks && ok; ++b) {
             const int w = b % Sh::NB;
             const bool kv = b + 1 < blocks || want_state;
@@ -560,7 +566,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
     } else if (warp == 3 && OUT) {
         // ------------------------------------------- issuer: S A^T and V^T P^T ----
         for (; issued < min(Sh::NS - 1, blocks); ++issued) load(issued);
-        wait_for_previous();
+        wait_here();
         for (int b = 0; b < blocks; ++b) {
             // block b - 1 is done, and its state product, which the other issuer committed:
             // its stage takes block b + 2 while S is on its way
@@ -621,7 +627,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             decay[j / 2] = make_float2(a0 >= 0 ? m->pw[max(a0, 0)] : 0.f, a1 >= 0 ? m->pw[max(a1, 0)] : 0.f);
         }
         for (int b = 0; b < blocks; ++b) {
-            if (b == 1) wait_for_previous();
+            if (b == 1) wait_here();
             if (!warp_wait(BAR(sc_full, b & 1), b >> 1, E_MMA)) break;
             if (b >= 2 && !warp_wait(BAR(done, (b - 2) % 3), (b - 2) / 3, E_MMA)) break;
             tc_fence_after();
