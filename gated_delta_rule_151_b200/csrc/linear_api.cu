@@ -147,6 +147,29 @@ struct Call {
     uint32_t used;   // status words handed out
     bool launched;   // a kernel of this call went before
     cudaError_t error;
+    struct {
+        const void *base;
+        int heads;
+        CUtensorMap map;
+    } maps[4];       // of the call's bf16 tensors: each is made once
+    int map_count;
+
+    void begin(const int32_t *cu_, const float *decay_, int N_, int T_, int H_, const Plan &plan_, const Layout &lay_,
+               void *ws_, bool bf16_, cudaStream_t stream_) {
+        cu = cu_; decay = decay_; N = N_; total_T = T_; H = H_; plan = plan_; lay = lay_;
+        ws = static_cast<uint8_t *>(ws_);
+        bf16 = bf16_; stream = stream_;
+        used = 0; launched = false; error = cudaSuccess; map_count = 0;
+    }
+
+    const CUtensorMap *map_of(const void *base, int heads) {
+        for (int i = 0; i < map_count; ++i)
+            if (maps[i].base == base && maps[i].heads == heads) return &maps[i].map;
+        if (map_count == 4 || !scan_tile_map(&maps[map_count].map, base, total_T, heads)) return nullptr;
+        maps[map_count].base = base;
+        maps[map_count].heads = heads;
+        return &maps[map_count++].map;
+    }
 
     // A scan's arguments; `buffer`: which states between segments it goes by.
     ScanArgs args(const void *a, int HA, const void *b, int HB, const void *v, int HV, const float *s_in,
@@ -181,8 +204,14 @@ struct Call {
         p.status_words = tc ? lay.words : 0;
         p.late = late;
         used += (uint32_t)(states ? plan.inner : plan.slots) * H;
-        error = tc ? launch_scan_tc(p, reverse, states, out_f32, launched, stream)
-                   : launch_scan_simt(p, d_b, d_v, reverse, states, bf16, out_f32, launched, stream);
+        if (tc) {
+            const CUtensorMap *a = map_of(p.a, p.HA), *b = map_of(p.b, p.HB), *v = map_of(p.v, p.HV);
+            error = a == nullptr || b == nullptr || v == nullptr
+                        ? cudaErrorInvalidValue
+                        : launch_scan_tc(*a, *b, *v, p, reverse, states, out_f32, launched, stream);
+        } else {
+            error = launch_scan_simt(p, d_b, d_v, reverse, states, bf16, out_f32, launched, stream);
+        }
         launched = true;
     }
     void join(const ScanArgs &p, int d_b, int d_v, bool reverse) {
@@ -261,8 +290,8 @@ gdr_status_t gdr_linear_prefill(const void *q, const void *k, const void *v, con
     if (!apart(in, out)) return GDR_ERR_INVALID_ARG;
     if (total_T == 0) return status_of(pass_state(final_state, initial_state, state, s));
 
-    Call c{cu_seqlens, decay, num_seqs, total_T, H, plan, lay, static_cast<uint8_t *>(workspace),
-           io_dtype == GDR_BF16, s, 0, false, cudaSuccess};
+    Call c;
+    c.begin(cu_seqlens, decay, num_seqs, total_T, H, plan, lay, workspace, io_dtype == GDR_BF16, s);
     // in place and in segments: the last segment of a sequence may end before its
     // first one has read the incoming state, which therefore moves aside
     if (initial_state != nullptr && initial_state == final_state && plan.inner > 0) {
@@ -348,8 +377,8 @@ gdr_status_t gdr_linear_backward(const void *q, const void *k, const void *v, co
     if (!apart(in, out)) return GDR_ERR_INVALID_ARG;
     if (total_T == 0) return status_of(pass_state(d_initial_state, d_final_state, state, s));
 
-    Call c{cu_seqlens, decay, num_seqs, total_T, H, plan, lay, static_cast<uint8_t *>(workspace),
-           io_dtype == GDR_BF16, s, 0, false, cudaSuccess};
+    Call c;
+    c.begin(cu_seqlens, decay, num_seqs, total_T, H, plan, lay, workspace, io_dtype == GDR_BF16, s);
     // heads that share a query/key head: each one's dq and dk in fp32, then their sums.
     // A pass follows one that it does not need, so that neither waits for the other's
     // end; the first output pass waits for all states, and vouches for them.

@@ -26,6 +26,7 @@
 // however many sequences there are.  dk and dv need the same states, one turned.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -136,8 +137,10 @@ __device__ inline Segment find_segment(const ScanArgs &p, int slot, bool inner, 
 
 // Launchers.  `states`: the pass that writes the segments' own states (all but
 // each sequence's last segment in scan order); otherwise the output pass.
-cudaError_t launch_scan_tc(const ScanArgs &p, bool reverse, bool states, bool out_f32, bool after,
-                           cudaStream_t stream);   // bf16, d_b = d_v = 128
+// (tensor cores: bf16, d_b = d_v = 128, with the tensors' tile maps)
+bool scan_tile_map(CUtensorMap *map, const void *base, int total_T, int H);
+cudaError_t launch_scan_tc(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &v, const ScanArgs &p,
+                           bool reverse, bool states, bool out_f32, bool after, cudaStream_t stream);
 cudaError_t launch_scan_simt(const ScanArgs &p, int d_b, int d_v, bool reverse, bool states,
                              bool bf16, bool out_f32, bool after, cudaStream_t stream);
 // Segments' own states -> states behind each segment, in place (after the states' pass).

@@ -689,20 +689,6 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
     }
 }
 
-// [T, H, 128] bf16 seen as {64 channels, T, 2 halves, H}: one box is a tile of 64
-// tokens by 128 channels of one head, its halves one after the other.
-bool make_tile_map(CUtensorMap *map, const void *base, int total_T, int H) {
-    auto enc = get_encode();
-    if (enc == nullptr) return false;
-    cuuint64_t dims[4] = {64, (cuuint64_t)total_T, 2, (cuuint64_t)H};
-    cuuint64_t strides[3] = {(cuuint64_t)H * D * 2, 128, (cuuint64_t)D * 2};
-    cuuint32_t box[4] = {64, C, 2, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <bool OUT, bool REV, typename OutT, bool TWO>
 cudaError_t launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mv,
                    const ScanArgs &p, bool after, cudaStream_t stream) {
@@ -722,12 +708,22 @@ cudaError_t launch_out(const CUtensorMap &ma, const CUtensorMap &mb, const CUten
 
 }  // namespace
 
-cudaError_t launch_scan_tc(const ScanArgs &p, bool reverse, bool states, bool out_f32, bool after,
-                           cudaStream_t stream) {
-    CUtensorMap ma, mb, mv;
-    if (!make_tile_map(&ma, p.a, p.total_T, p.HA) || !make_tile_map(&mb, p.b, p.total_T, p.HB) ||
-        !make_tile_map(&mv, p.v, p.total_T, p.HV))
-        return cudaErrorInvalidValue;
+// [T, H, 128] bf16 seen as {64 channels, T, 2 halves, H}: one box is a tile of 64
+// tokens by 128 channels of one head, its halves one after the other.
+bool scan_tile_map(CUtensorMap *map, const void *base, int total_T, int H) {
+    auto enc = get_encode();
+    if (enc == nullptr) return false;
+    cuuint64_t dims[4] = {64, (cuuint64_t)total_T, 2, (cuuint64_t)H};
+    cuuint64_t strides[3] = {(cuuint64_t)H * D * 2, 128, (cuuint64_t)D * 2};
+    cuuint32_t box[4] = {64, C, 2, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_scan_tc(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mv, const ScanArgs &p,
+                           bool reverse, bool states, bool out_f32, bool after, cudaStream_t stream) {
     if (states)
         return reverse ? launch<false, true, float, false>(ma, mb, mv, p, after, stream)
                        : launch<false, false, float, false>(ma, mb, mv, p, after, stream);
