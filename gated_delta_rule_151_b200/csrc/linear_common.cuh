@@ -64,7 +64,7 @@ struct Segment {
 };
 
 __host__ __device__ inline int segments_of(int len, int seg_tokens) {
-    return len <= seg_tokens ? 1 : (len + seg_tokens - 1) / seg_tokens;
+    return len <= seg_tokens ? 1 : 1 + (len - 1) / seg_tokens;
 }
 
 // The segment of a slot, or with `inner` of a state between segments.  Called
