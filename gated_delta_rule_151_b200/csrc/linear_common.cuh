@@ -124,8 +124,9 @@ __device__ inline Segment find_segment(const ScanArgs &p, int slot, bool inner, 
     s.seq_len = len;
     s.count = segments_of(len, p.seg_tokens);
     s.state = inner ? slot : slot - s.n;
-    // a cu_seqlens that is no partition may count more segments than there is room for
-    if ((unsigned)s.index >= (unsigned)s.count || s.state > p.inner) {
+    // a cu_seqlens that is no partition may count more segments than there is room for,
+    // or than an int holds
+    if ((unsigned)s.index >= (unsigned)s.count || s.state > p.inner || (!inner && s.state < s.index)) {
         s.n = -1;
         return s;
     }

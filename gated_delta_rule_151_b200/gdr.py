@@ -599,6 +599,13 @@ def _given(t, name, shape, dtype, device):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _int32(n, name):
+    """n, which ctypes would otherwise cut to 32 bits."""
+    if not -(1 << 31) <= n < 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits, got {n}")
+    return n
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
 
@@ -634,7 +641,7 @@ def _linear_args(q, k, v, decay, cu_seqlens, num_seqs):
         if num_seqs is not None and int(num_seqs) != N:
             raise ValueError(f"num_seqs is {num_seqs}, cu_seqlens has {N} sequences")
     else:
-        N = 1 if num_seqs is None else int(num_seqs)
+        N = 1 if num_seqs is None else _int32(int(num_seqs), "num_seqs")
     return T, Hqk, H, dk, dv, N, dev, io
 
 
@@ -648,6 +655,9 @@ def _linear_bytes(*shape):
 
 def gdr_linear_workspace_size(num_seqs, total_T, H_qk, H, d_k, d_v, io_dtype,
                               backward=False) -> int:
+    for n, name in ((num_seqs, "num_seqs"), (total_T, "total_T"), (H_qk, "H_qk"), (H, "H"), (d_k, "d_k"),
+                    (d_v, "d_v")):
+        _int32(n, name)
     return _linear_bytes(num_seqs, total_T, H_qk, H, d_k, d_v, io_dtype, int(backward))
 
 
@@ -764,7 +774,7 @@ def _norm_args(x, weight, gate, residual, next_weight, activation):
     act = _ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, got {activation!r}")
-    dim, dev, io = shape[-1], x.device, x.dtype
+    dim, dev, io = _int32(shape[-1], "x's last dimension"), x.device, x.dtype
     if gate is not None:
         _given(gate, "gate", shape, io, dev)
     if residual is not None:
@@ -818,7 +828,7 @@ def _norm_bytes(rows, dim):
 
 
 def gdr_norm_gate_workspace_size(rows, dim) -> int:
-    return _norm_bytes(rows, dim)
+    return _norm_bytes(rows, _int32(dim, "dim"))
 
 
 def gdr_norm_gate_backward(x, dy=None, dn=None, weight=None, gate=None, residual=None,

@@ -468,8 +468,8 @@ GDR_API gdr_status_t gdr_backward(const void *q, const void *k, const void *v, c
  *
  * bf16 with d_k = d_v = 128 runs on the tensor cores: 64-token blocks, the
  * copy of the state that meets the queries and (with more than 4096 outputs of
- * d_v values) the scores rounded to bf16, the state itself fp32 throughout.  Other shapes and fp32 run in fp32
- * on the CUDA cores.  Infinities and NaN stay inside their (sequence, head);
+ * d_v values) the scores rounded to bf16, the state itself fp32 throughout.
+ * Other shapes and fp32 run in fp32 on the CUDA cores.  Infinities and NaN stay inside their (sequence, head);
  * a non-finite value in v or k leaves NaN in every later output it reaches.
  *
  * cu_seqlens, initial_state, final_state (which may be initial_state) and
@@ -513,7 +513,8 @@ GDR_API gdr_status_t gdr_linear_backward(const void *q, const void *k, const voi
  * After a gdr_linear_prefill or gdr_linear_backward with this workspace:
  * whether a bounded device-side wait in it gave up (GDR_ERR_DEVICE_TIMEOUT;
  * its outputs are then not valid) or not (GDR_OK).  Synchronises `stream` and
- * copies the call's status words.
+ * copies the call's status words.  A call without tokens uses no workspace and
+ * leaves none of this in it.
  */
 GDR_API gdr_status_t gdr_linear_check_workspace(const void *workspace, size_t workspace_bytes,
                                                 void *stream);

@@ -132,3 +132,13 @@ def test_binding_refuses_before_the_library():
         gdr.gdr_linear_prefill(x, x, x, torch.zeros(2))        # not on a GPU
     with pytest.raises(ValueError):
         gdr.gdr_norm_gate(x)
+
+
+@pytest.mark.parametrize("size", [
+    lambda n: gdr.gdr_linear_workspace_size(n + 1, 64, 2, 2, 16, 16, 0), lambda n: gdr.gdr_linear_workspace_size(1, n + 64, 2, 2, 16, 16, 0),
+    lambda n: gdr.gdr_linear_workspace_size(1, 64, 2, n + 2, 16, 16, 0), lambda n: gdr.gdr_norm_gate_workspace_size(4, n + 128)])
+def test_binding_refuses_sizes_beyond_32_bits(size):
+    """Whole multiples of 2^32 beside a good size: cut to 32 bits they would pass for it."""
+    assert size(0) >= 0
+    with pytest.raises(ValueError):
+        size(1 << 32)
