@@ -64,19 +64,32 @@ __device__ __forceinline__ void store_piece(__nv_bfloat16 *p, const float (&f)[8
 // the value.  The full-precision pair took the heads' forward pass from 23 to 35 us.
 __device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.0f + ex2_approx(-kLog2e * z)); }
 
-// act(z) and, for the gradient, act'(z).
-__device__ __forceinline__ float act_of(int act, float z) {
-    return act == kActSilu ? z * sigmoid(z) : act == kActSigmoid ? sigmoid(z) : z;
+// act(z) in place of z and, for the gradient, act'(z), of a piece.  The choice stands
+// outside the channels' loops, whose exponentials then overlap.
+template <int E>
+__device__ __forceinline__ void act_of(int act, float (&z)[E]) {
+    if (act == kActNone) return;
+    const bool silu = act == kActSilu;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const float s = sigmoid(z[e]);
+        z[e] = s * (silu ? z[e] : 1.f);
+    }
 }
-__device__ __forceinline__ void act_both(int act, float z, float &a, float &da) {
+template <int E>
+__device__ __forceinline__ void act_both(int act, float (&z)[E], float (&da)[E]) {
     if (act == kActNone) {
-        a = z;
-        da = 1.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) da[e] = 1.f;
         return;
     }
-    const float s = sigmoid(z);
-    a = act == kActSilu ? z * s : s;
-    da = act == kActSilu ? s * (1.f + z * (1.f - s)) : s * (1.f - s);
+    const bool silu = act == kActSilu;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const float s = sigmoid(z[e]), rest = 1.f - s;
+        da[e] = s * (silu ? fmaf(z[e], rest, 1.f) : rest);
+        z[e] = s * (silu ? z[e] : 1.f);
+    }
 }
 
 // Sum over the TPR threads of a row; every thread of the block takes part.
@@ -109,7 +122,6 @@ __device__ __forceinline__ void row_sum(float (&x)[NV], float *scratch, int &tur
     }
 }
 
-constexpr int kStages = 2;   // row groups a block holds: one at work, one on its way (three gained nothing)
 constexpr int kMostRing = 200 * 1024;
 
 template <typename T, int TPR, int VPT>
@@ -117,6 +129,12 @@ struct Shape {
     static constexpr int NT = TPR > 256 ? TPR : 256;
     static constexpr int ROWS = NT / TPR;                  // rows of a block at a time
     static constexpr int E = 16 / sizeof(T);
+    // Row groups a block holds, one at work and the others on their way.  A third helps
+    // the gradient (8191 x 2048 fp32: 97 -> 86 us; a fourth nothing) and costs the forward
+    // pass resident blocks (131,072 x 128 bf16: 18.7 -> 20.0).
+    static constexpr int stages(bool back, int tensors) {
+        return back && 3 * tensors * VPT * NT * 16 <= kMostRing ? 3 : 2;
+    }
 };
 
 // A thread's pieces of the next row groups, copied to shared memory without
@@ -124,10 +142,10 @@ struct Shape {
 // itself: no barriers.  `Tensors` rows side by side.  Rows too wide for it (fp32
 // gradients beyond 4096 channels, every row beyond 8192) are read from memory where they
 // are used.
-template <typename T, int TPR, int VPT, int Tensors>
+template <typename T, int TPR, int VPT, int Tensors, int Stages>
 struct Ring {
     using Sh = Shape<T, TPR, VPT>;
-    static constexpr int WANTED = kStages * Tensors * VPT * Sh::NT * 16;
+    static constexpr int WANTED = Stages * Tensors * VPT * Sh::NT * 16;
     static constexpr bool STAGED = WANTED <= kMostRing;
     static constexpr int BYTES = STAGED ? WANTED : 0;
     uint32_t base;
@@ -157,7 +175,7 @@ struct Ring {
         }
     }
     static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-    static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory"); }
+    static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(Stages - 1) : "memory"); }
 };
 
 // GATE: a gate is given; NEXT: next_weight is.
@@ -165,10 +183,11 @@ template <typename T, int TPR, int VPT, bool GATE, bool NEXT>
 __global__ void __launch_bounds__(Shape<T, TPR, VPT>::NT)
 norm_gate_kernel(const NormArgs p) {
     using Sh = Shape<T, TPR, VPT>;
+    constexpr int kStages = Sh::stages(false, 2 + GATE);
     constexpr int E = Sh::E;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float scratch[64];
-    const Ring<T, TPR, VPT, 2 + GATE> ring{static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * 16};
+    const Ring<T, TPR, VPT, 2 + GATE, kStages> ring{static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * 16};
     int turn = 0;
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
     const int pieces = p.dim / E;
@@ -230,12 +249,15 @@ norm_gate_kernel(const NormArgs p) {
             if (live && c < pieces) {
                 float z[E], res[E];
                 const int64_t at = row * p.dim + c * E;
-                if (GATE) ring.read(stage, 1 + GATE, i, z_ + at, z);
+                if (GATE) {
+                    ring.read(stage, 1 + GATE, i, z_ + at, z);
+                    act_of(p.act, z);
+                }
                 if (res_ != nullptr) ring.read(stage, 1, i, res_ + at, res);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     float u = y[i][e] * r * w[i][e];
-                    if (GATE) u *= act_of(p.act, z[e]);
+                    if (GATE) u *= z[e];
                     y[i][e] = res_ != nullptr ? fmaf(p.scale, u, res[e]) : p.scale * u;
                     if (NEXT) s2[0] = fmaf(y[i][e], y[i][e], s2[0]);
                 }
@@ -259,15 +281,22 @@ norm_gate_kernel(const NormArgs p) {
     }
 }
 
+// Blocks an SM has to have room for: 80 registers a thread hold a piece's gradient without
+// the second norm (131,072 x 128: 39 -> 37 us against 128), with it they spill (59 -> 79).
+constexpr int backward_blocks(int threads_per_row, int pieces, bool next) {
+    return threads_per_row > 256 || pieces > 2 ? 1 : pieces > 1 || next ? 2 : 3;
+}
+
 // GATE: a gate is given; NEXT: dn is (and next_weight).
 template <typename T, int TPR, int VPT, bool GATE, bool NEXT>
-__global__ void __launch_bounds__(Shape<T, TPR, VPT>::NT, TPR > 256 || VPT > 2 ? 1 : 2)
+__global__ void __launch_bounds__(Shape<T, TPR, VPT>::NT, backward_blocks(TPR, VPT, NEXT))
 norm_gate_backward_kernel(const NormArgs p) {
     using Sh = Shape<T, TPR, VPT>;
+    constexpr int kStages = Sh::stages(true, 2 + GATE + 2 * NEXT);
     constexpr int E = Sh::E;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float scratch[64];
-    const Ring<T, TPR, VPT, 2 + GATE + 2 * NEXT> ring{static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * 16};
+    const Ring<T, TPR, VPT, 2 + GATE + 2 * NEXT, kStages> ring{static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * 16};
     int turn = 0;
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
     const int pieces = p.dim / E;
@@ -292,15 +321,39 @@ norm_gate_backward_kernel(const NormArgs p) {
         }
         ring.commit();
     };
-    float dw[VPT][E], dw2[VPT][E], w[VPT][E], w2[VPT][E];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
+    // the weights stay in registers as far as there is room beside their gradients; wider
+    // rows read them again from the caches where they are used
+    constexpr bool KEPT = VPT * E <= 8;
+    auto load_w = [&](int i, float (&f)[E]) {
         const int c = lane + i * TPR;
 #pragma unroll
-        for (int e = 0; e < E; ++e) { dw[i][e] = dw2[i][e] = 0.f; w[i][e] = 1.f; w2[i][e] = 0.f; }
-        if (c < pieces && p.weight != nullptr) load_weights(p.weight + c * E, w[i]);
-        if (c < pieces && NEXT) load_weights(p.next_weight + c * E, w2[i]);
+        for (int e = 0; e < E; ++e) f[e] = 1.f;
+        if (c < pieces && p.weight != nullptr) load_weights(p.weight + c * E, f);
+    };
+    auto load_w2 = [&](int i, float (&f)[E]) {
+        const int c = lane + i * TPR;
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = 0.f;
+        if (c < pieces && NEXT) load_weights(p.next_weight + c * E, f);
+    };
+    float dw[VPT][E], dw2[VPT][E], kept_w[VPT][E], kept_w2[VPT][E];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) dw[i][e] = dw2[i][e] = 0.f;
+        load_w(i, kept_w[i]);
+        load_w2(i, kept_w2[i]);
     }
+    auto weights = [&](int i, float (&f)[E]) {
+        if (!KEPT) return load_w(i, f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = kept_w[i][e];
+    };
+    auto next_weights = [&](int i, float (&f)[E]) {
+        if (!KEPT) return load_w2(i, f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = kept_w2[i][e];
+    };
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) fetch(first + s * stride, s);
     int stage = 0;
@@ -333,17 +386,17 @@ norm_gate_backward_kernel(const NormArgs p) {
         float a[VPT][E], da[VPT][E];           // act(z) and act'(z)
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            float z[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) z[e] = 0.f;
-            if (GATE && live && lane + i * TPR < pieces) ring.read(stage, 2, i, z_ + at + (lane + i * TPR) * E, z);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                a[i][e] = 1.f;
+                a[i][e] = GATE ? 0.f : 1.f;
                 da[i][e] = 0.f;
-                if (GATE) act_both(p.act, z[e], a[i][e], da[i][e]);
-                x[i][e] *= r;                  // xh
             }
+            if (GATE && live && lane + i * TPR < pieces) {
+                ring.read(stage, 2, i, z_ + at + (lane + i * TPR) * E, a[i]);
+                act_both(p.act, a[i], da[i]);
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[i][e] *= r;          // xh
         }
         if (NEXT) {
             // y again, and the two sums of the second norm
@@ -356,26 +409,32 @@ norm_gate_backward_kernel(const NormArgs p) {
                 const int64_t here = at + (lane + i * TPR) * E;
                 if (in) ring.read(stage, 2 + GATE, i, dn_ + here, t[i]);
                 if (in && res_ != nullptr) ring.read(stage, 3 + GATE, i, res_ + here, y[i]);
+                float w[E], w2[E];
+                weights(i, w);
+                next_weights(i, w2);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    float u = x[i][e] * w[i][e];
+                    float u = x[i][e] * w[e];
                     if (GATE) u *= a[i][e];
                     y[i][e] = fmaf(p.scale, u, y[i][e]);
                     s[0] = fmaf(y[i][e], y[i][e], s[0]);
-                    s[1] = fmaf(t[i][e] * w2[i][e], y[i][e], s[1]);
+                    s[1] = fmaf(t[i][e] * w2[e], y[i][e], s[1]);
                 }
             }
             row_sum<TPR>(s, scratch, turn);
             const float r2 = rsqrtf(s[0] * p.inv_dim + p.eps);
             const float m = s[1] * r2 * p.inv_dim;       // mean(dn w2 yh)
 #pragma unroll
-            for (int i = 0; i < VPT; ++i)
+            for (int i = 0; i < VPT; ++i) {
+                float w2[E];
+                next_weights(i, w2);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     const float yh = y[i][e] * r2;
                     dw2[i][e] = fmaf(t[i][e], yh, dw2[i][e]);
-                    g[i][e] = fmaf(r2, fmaf(-yh, m, t[i][e] * w2[i][e]), g[i][e]);
+                    g[i][e] = fmaf(r2, fmaf(-yh, m, t[i][e] * w2[e]), g[i][e]);
                 }
+            }
         }
         float s[1] = {0.f};
 #pragma unroll
@@ -383,13 +442,14 @@ norm_gate_backward_kernel(const NormArgs p) {
             const int c = lane + i * TPR;
             const bool in = live && c < pieces;
             if (in && p.dresidual != nullptr) store_piece(static_cast<T *>(p.dresidual) + at + c * E, g[i]);
-            float dz[E];
+            float dz[E], w[E];
+            weights(i, w);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const float du = p.scale * g[i][e], dua = du * a[i][e];
-                dz[e] = du * x[i][e] * w[i][e] * da[i][e];
+                dz[e] = du * x[i][e] * w[e] * da[i][e];
                 dw[i][e] = fmaf(dua, x[i][e], dw[i][e]);
-                g[i][e] = dua * w[i][e];
+                g[i][e] = dua * w[e];
                 s[0] = fmaf(g[i][e], x[i][e], s[0]);
             }
             if (GATE && in) store_piece(static_cast<T *>(p.dgate) + at + c * E, dz);
@@ -487,7 +547,8 @@ template <typename T, bool BACK, int TPR, int VPT, bool GATE, bool NEXT>
 cudaError_t launch_as(const NormArgs &p, cudaStream_t s) {
     using Sh = Shape<T, TPR, VPT>;
     auto kernel = BACK ? norm_gate_backward_kernel<T, TPR, VPT, GATE, NEXT> : norm_gate_kernel<T, TPR, VPT, GATE, NEXT>;
-    constexpr int bytes = BACK ? Ring<T, TPR, VPT, 2 + GATE + 2 * NEXT>::BYTES : Ring<T, TPR, VPT, 2 + GATE>::BYTES;
+    constexpr int tensors = BACK ? 2 + GATE + 2 * NEXT : 2 + GATE;
+    constexpr int bytes = Ring<T, TPR, VPT, tensors, Sh::stages(BACK, tensors)>::BYTES;
     static std::atomic<int> resident{0};
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), bytes);
     if (e != cudaSuccess) return e;
