@@ -60,6 +60,14 @@ __device__ __forceinline__ void store_piece(__nv_bfloat16 *p, const float (&f)[8
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Two channels at a time: the gradient's arithmetic took half of its issue slots
+// (131,072 x 128 bf16: 34.4 -> 32.4 us; 4096 x 8192: 214 -> 178).
+__device__ __forceinline__ float2 two(const float *f) { return make_float2(f[0], f[1]); }
+__device__ __forceinline__ float2 two(float f) { return make_float2(f, f); }
+__device__ __forceinline__ void put2(float *f, float2 x) { f[0] = x.x; f[1] = x.y; }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
 // Single-instruction exponential and reciprocal: together within 2^-21 (1 + |z| / 8) of
 // the value.  The full-precision pair took the heads' forward pass from 23 to 35 us.
 __device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.0f + ex2_approx(-kLog2e * z)); }
@@ -282,9 +290,10 @@ norm_gate_kernel(const NormArgs p) {
 }
 
 // Blocks an SM has to have room for: 80 registers a thread hold a piece's gradient without
-// the second norm (131,072 x 128: 39 -> 37 us against 128), with it they spill (59 -> 79).
+// the second norm (131,072 x 128 bf16: 39 -> 37 us against 128), with it they spill (8192 x
+// 2048: 59 -> 79).  Two fp32 pieces with it fill the ring of the only block.
 constexpr int backward_blocks(int threads_per_row, int pieces, bool next) {
-    return threads_per_row > 256 || pieces > 2 ? 1 : pieces > 1 || next ? 2 : 3;
+    return threads_per_row > 256 || pieces > 2 || (pieces > 1 && next) ? 1 : pieces > 1 || next ? 2 : 3;
 }
 
 // GATE: a gate is given; NEXT: dn is (and next_weight).
@@ -375,11 +384,12 @@ norm_gate_backward_kernel(const NormArgs p) {
         }
         float r = 1.f;
         if (p.weight != nullptr) {
-            float s[1] = {0.f};
+            float2 ss = two(0.f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int e = 0; e < E; ++e) s[0] = fmaf(x[i][e], x[i][e], s[0]);
+                for (int e = 0; e < E; e += 2) ss = fma2(two(&x[i][e]), two(&x[i][e]), ss);
+            float s[1] = {ss.x + ss.y};
             row_sum<TPR>(s, scratch, turn);
             r = rsqrtf(s[0] * p.inv_dim + p.eps);
         }
@@ -396,11 +406,12 @@ norm_gate_backward_kernel(const NormArgs p) {
                 act_both(p.act, a[i], da[i]);
             }
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[i][e] *= r;          // xh
+            for (int e = 0; e < E; e += 2) put2(&x[i][e], mul2(two(&x[i][e]), two(r)));          // xh
         }
         if (NEXT) {
             // y again, and the two sums of the second norm
-            float s[2] = {0.f, 0.f}, y[VPT][E], t[VPT][E];
+            float y[VPT][E], t[VPT][E];
+            float2 sy = two(0.f), st = sy;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const bool in = live && lane + i * TPR < pieces;
@@ -413,14 +424,16 @@ norm_gate_backward_kernel(const NormArgs p) {
                 weights(i, w);
                 next_weights(i, w2);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    float u = x[i][e] * w[e];
-                    if (GATE) u *= a[i][e];
-                    y[i][e] = fmaf(p.scale, u, y[i][e]);
-                    s[0] = fmaf(y[i][e], y[i][e], s[0]);
-                    s[1] = fmaf(t[i][e] * w2[e], y[i][e], s[1]);
+                for (int e = 0; e < E; e += 2) {
+                    float2 u = mul2(two(&x[i][e]), two(&w[e]));
+                    if (GATE) u = mul2(u, two(&a[i][e]));
+                    const float2 yy = fma2(two(p.scale), u, two(&y[i][e]));
+                    put2(&y[i][e], yy);
+                    sy = fma2(yy, yy, sy);
+                    st = fma2(mul2(two(&t[i][e]), two(&w2[e])), yy, st);
                 }
             }
+            float s[2] = {sy.x + sy.y, st.x + st.y};
             row_sum<TPR>(s, scratch, turn);
             const float r2 = rsqrtf(s[0] * p.inv_dim + p.eps);
             const float m = s[1] * r2 * p.inv_dim;       // mean(dn w2 yh)
@@ -429,14 +442,14 @@ norm_gate_backward_kernel(const NormArgs p) {
                 float w2[E];
                 next_weights(i, w2);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float yh = y[i][e] * r2;
-                    dw2[i][e] = fmaf(t[i][e], yh, dw2[i][e]);
-                    g[i][e] = fmaf(r2, fmaf(-yh, m, t[i][e] * w2[e]), g[i][e]);
+                for (int e = 0; e < E; e += 2) {
+                    const float2 yh = mul2(two(&y[i][e]), two(r2)), tt = two(&t[i][e]);
+                    put2(&dw2[i][e], fma2(tt, yh, two(&dw2[i][e])));
+                    put2(&g[i][e], fma2(two(r2), fma2(yh, two(-m), mul2(tt, two(&w2[e]))), two(&g[i][e])));
                 }
             }
         }
-        float s[1] = {0.f};
+        float2 sg = two(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = lane + i * TPR;
@@ -445,15 +458,18 @@ norm_gate_backward_kernel(const NormArgs p) {
             float dz[E], w[E];
             weights(i, w);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float du = p.scale * g[i][e], dua = du * a[i][e];
-                dz[e] = du * x[i][e] * w[e] * da[i][e];
-                dw[i][e] = fmaf(dua, x[i][e], dw[i][e]);
-                g[i][e] = dua * w[e];
-                s[0] = fmaf(g[i][e], x[i][e], s[0]);
+            for (int e = 0; e < E; e += 2) {
+                const float2 xh = two(&x[i][e]), ww = two(&w[e]);
+                const float2 du = mul2(two(p.scale), two(&g[i][e])), dua = GATE ? mul2(du, two(&a[i][e])) : du;
+                if (GATE) put2(&dz[e], mul2(mul2(mul2(du, xh), ww), two(&da[i][e])));
+                put2(&dw[i][e], fma2(dua, xh, two(&dw[i][e])));
+                const float2 t = mul2(dua, ww);
+                put2(&g[i][e], t);
+                sg = fma2(t, xh, sg);
             }
             if (GATE && in) store_piece(static_cast<T *>(p.dgate) + at + c * E, dz);
         }
+        float s[1] = {sg.x + sg.y};
         if (p.weight != nullptr) row_sum<TPR>(s, scratch, turn);
         const float m = p.weight != nullptr ? s[0] * p.inv_dim : 0.f;
 #pragma unroll
@@ -461,7 +477,7 @@ norm_gate_backward_kernel(const NormArgs p) {
             const int c = lane + i * TPR;
             if (live && c < pieces) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) x[i][e] = r * fmaf(-x[i][e], m, g[i][e]);
+                for (int e = 0; e < E; e += 2) put2(&x[i][e], mul2(two(r), fma2(two(&x[i][e]), two(-m), two(&g[i][e]))));
                 store_piece(static_cast<T *>(p.dx) + at + c * E, x[i]);
             }
         }
