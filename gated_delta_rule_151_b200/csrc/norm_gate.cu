@@ -60,8 +60,8 @@ __device__ __forceinline__ void store_piece(__nv_bfloat16 *p, const float (&f)[8
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Two channels at a time: the gradient's arithmetic took half of its issue slots
-// (131,072 x 128 bf16: 34.4 -> 32.4 us; 4096 x 8192: 214 -> 178).
+// Two channels at a time: the arithmetic took half of the issue slots and more (131,072 x
+// 128 bf16: 17.7 -> 17.1 us, its gradient 34.4 -> 32.4; 4096 x 8192: gradient 214 -> 178).
 __device__ __forceinline__ float2 two(const float *f) { return make_float2(f[0], f[1]); }
 __device__ __forceinline__ float2 two(float f) { return make_float2(f, f); }
 __device__ __forceinline__ void put2(float *f, float2 x) { f[0] = x.x; f[1] = x.y; }
@@ -139,7 +139,7 @@ struct Shape {
     static constexpr int E = 16 / sizeof(T);
     // Row groups a block holds, one at work and the others on their way.  A third helps
     // the gradient (8191 x 2048 fp32: 97 -> 86 us; a fourth nothing) and costs the forward
-    // pass resident blocks (131,072 x 128 bf16: 18.7 -> 20.0).
+    // pass resident blocks (131,072 x 128 bf16: 18.7 -> 20.0 before the packed arithmetic).
     static constexpr int stages(bool back, int tensors) {
         return back && 3 * tensors * VPT * NT * 16 <= kMostRing ? 3 : 2;
     }
@@ -242,15 +242,16 @@ norm_gate_kernel(const NormArgs p) {
         }
         float r = 1.f;
         if (p.weight != nullptr) {
-            float s[1] = {0.f};
+            float2 ss = two(0.f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int e = 0; e < E; ++e) s[0] = fmaf(y[i][e], y[i][e], s[0]);
+                for (int e = 0; e < E; e += 2) ss = fma2(two(&y[i][e]), two(&y[i][e]), ss);
+            float s[1] = {ss.x + ss.y};
             row_sum<TPR>(s, scratch, turn);
             r = rsqrtf(s[0] * p.inv_dim + p.eps);
         }
-        float s2[1] = {0.f};
+        float2 sy = two(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = lane + i * TPR;
@@ -261,18 +262,22 @@ norm_gate_kernel(const NormArgs p) {
                     ring.read(stage, 1 + GATE, i, z_ + at, z);
                     act_of(p.act, z);
                 }
+#pragma unroll
+                for (int e = 0; e < E; ++e) res[e] = 0.f;
                 if (res_ != nullptr) ring.read(stage, 1, i, res_ + at, res);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    float u = y[i][e] * r * w[i][e];
-                    if (GATE) u *= z[e];
-                    y[i][e] = res_ != nullptr ? fmaf(p.scale, u, res[e]) : p.scale * u;
-                    if (NEXT) s2[0] = fmaf(y[i][e], y[i][e], s2[0]);
+                for (int e = 0; e < E; e += 2) {
+                    float2 u = mul2(mul2(two(&y[i][e]), two(r)), two(&w[i][e]));
+                    if (GATE) u = mul2(u, two(&z[e]));
+                    const float2 yy = fma2(two(p.scale), u, two(&res[e]));
+                    put2(&y[i][e], yy);
+                    if (NEXT) sy = fma2(yy, yy, sy);
                 }
                 store_piece(static_cast<T *>(p.y) + row * p.dim + c * E, y[i]);
             }
         }
         if (NEXT) {
+            float s2[1] = {sy.x + sy.y};
             row_sum<TPR>(s2, scratch, turn);
             const float r2 = rsqrtf(s2[0] * p.inv_dim + p.eps);
 #pragma unroll
@@ -280,7 +285,7 @@ norm_gate_kernel(const NormArgs p) {
                 const int c = lane + i * TPR;
                 if (live && c < pieces) {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) y[i][e] *= r2 * w2[i][e];
+                    for (int e = 0; e < E; e += 2) put2(&y[i][e], mul2(two(&y[i][e]), mul2(two(r2), two(&w2[i][e]))));
                     store_piece(static_cast<T *>(p.y_norm) + row * p.dim + c * E, y[i]);
                 }
             }
