@@ -177,3 +177,27 @@ def test_no_rows():
     assert y.shape == n.shape == (0, 128)
     got = gdr.gdr_norm_gate_backward(c["x"], c["dy"], c["dn"], *(c[k] for k in FULL))
     assert (got[1] == 0).all() and (got[4] == 0).all() and got[0].shape == (0, 128)
+
+
+@pytest.mark.parametrize("second", [True, False], ids=["next", "alone"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows,dim", [(700, 8192), (1500, 4096), (4001, 2048), (50000, 128)])
+def test_blocks_of_many_rows(rows, dim, dtype, second):
+    """Four row groups and more for each block, so that every place of its ring is used again."""
+    parts = FULL if second else FULL[:2]
+    c = make(rows, dim, dtype, parts + ("dy", "dn"), seed=7)
+    d = gpu(c)
+    arg = {k: d[k] for k in parts}
+    out = gdr.gdr_norm_gate(d["x"], **arg, scale=0.5, eps=EPS)
+    got = gdr.gdr_norm_gate_backward(d["x"], d["dy"], d["dn"] if second else None, **arg, scale=0.5, eps=EPS)
+    leaves = {k: d[k].double().requires_grad_() for k in ("x",) + parts}
+    y, n = ref.norm_gate(leaves["x"], *(leaves.get(k) for k in FULL), 0.5, EPS, "silu")
+    loss = (y * d["dy"].double()).sum() + ((n * d["dn"].double()).sum() if second else 0)
+    want = dict(zip(leaves, torch.autograd.grad(loss, list(leaves.values()))))
+    tol = step(dtype) if dtype == torch.bfloat16 else 1e-5
+    assert relative(out[0], y.detach().cpu()) <= tol
+    assert not second or relative(out[1], n.detach().cpu()) <= tol
+    for k, r in zip(("x", "weight", "gate", "residual", "next_weight"), got):
+        assert (r is None) == (k not in want), k
+        if r is not None:
+            assert relative(r, want[k].cpu()) <= (step(dtype) if r.dtype == torch.bfloat16 else 1e-5), k
