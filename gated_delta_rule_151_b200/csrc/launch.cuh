@@ -6,12 +6,12 @@
 namespace gdr {
 
 // The kernels of one call follow each other without draining the GPU between them:
-// each lets the next one start once its own blocks have, and waits for the one
-// before to be complete where it first touches memory that passes between them.
+// each lets the next one start once its own blocks have, and every thread that reads
+// what an earlier kernel of the call wrote waits for the one before to be complete
+// first (the wait also makes those writes visible to its grid; nothing else does).
 // Every kernel launched with `after` waits in every block that has work, at its
 // start or at its end, so a kernel is complete only when all before it in the call
-// are.  One that lets the next one start only after its own wait vouches for what
-// came before it: the next need not wait for that again.
+// are.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

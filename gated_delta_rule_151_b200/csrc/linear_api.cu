@@ -380,8 +380,8 @@ gdr_status_t gdr_linear_backward(const void *q, const void *k, const void *v, co
     Call c;
     c.begin(cu_seqlens, decay, num_seqs, total_T, H, plan, lay, workspace, io_dtype == GDR_BF16, s);
     // heads that share a query/key head: each one's dq and dk in fp32, then their sums.
-    // A pass follows one that it does not need, so that neither waits for the other's
-    // end; the first output pass waits for all states, and vouches for them.
+    // A pass follows one that it does not need, so that the segments that enter with the
+    // caller's state need not wait for the other's end.
     const bool group = H != H_qk;
     float *part[2] = {reinterpret_cast<float *>(c.ws + lay.part[0]), reinterpret_cast<float *>(c.ws + lay.part[1])};
     const ScanArgs pq = c.args(d_o, H, v, H, k, H_qk, initial_state, true, nullptr, group ? part[0] : dq, 0, false);

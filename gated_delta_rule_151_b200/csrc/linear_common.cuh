@@ -51,7 +51,7 @@ struct ScanArgs {
     int seg_tokens;                  // multiple of kScanBlock
     int slots, inner;                // segments, and those that are not their sequence's last
     int turned, seg_turned;          // s_in, the states between segments are stored [d_b, d_v]
-    int late;                        // output pass behind another one whose results it does not need
+    int late;                        // output pass behind another one: needs none of its results, but the states from before it
 };
 
 struct Segment {

@@ -51,12 +51,14 @@ scan_simt_kernel(const ScanArgs p) {
     __shared__ int scratch[34];
     const int tid = threadIdx.x;
     const int slot = blockIdx.x / p.H, h = blockIdx.x % p.H;
-    if (!OUT) launch_dependents();
+    launch_dependents();
     if (!OUT || !p.late) wait_for_previous();
-    if (OUT) launch_dependents();     // (an output pass behind this one goes by what this one waited for)
     if (OUT && blockIdx.x == 0 && tid == 0) *p.header = p.status_words;
     const Segment seg = find_segment(p, slot, !OUT, REV, scratch, NT);
     if (seg.n < 0) return;
+    // a late pass runs beside the one before, but not where it reads the states between segments
+    const bool beside = OUT && p.late && seg.index == 0;
+    if (OUT && p.late && !beside) wait_for_previous();
     const bool last = seg.index == seg.count - 1;
     const int ha = h / (p.H / p.HA), hb = h / (p.H / p.HB), hv = h / (p.H / p.HV);
     if (tid <= kTok) pw[tid] = expf(clamp_log_gate(p.decay[h]) * (float)tid);
@@ -232,7 +234,7 @@ scan_simt_kernel(const ScanArgs p) {
         }
         buf = after;
     }
-    if (OUT && p.late) wait_for_previous();
+    if (beside) wait_for_previous();
     float *out_state = OUT ? (last ? p.s_out : nullptr) : p.seg;
     if (used && out_state != nullptr) {
         float4 *dst = reinterpret_cast<float4 *>(out_state + (OUT ? state_at : ((size_t)seg.state * p.H + h) * (DV * DB)));

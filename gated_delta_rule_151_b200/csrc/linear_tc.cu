@@ -263,10 +263,12 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         __syncwarp();
         if (blocks > 0) load(issued++);
     }
-    // (an output pass behind this one goes by what this one waits for)
-    if (!OUT || p.late) launch_dependents();
+    launch_dependents();
+    // A pass whose inputs are all the caller's runs beside the one before; the states
+    // between segments are not.
+    const bool beside = !OUT || (p.late && seg.index == 0);
     auto wait_here = [&]() {
-        if (OUT && !p.late) wait_for_previous();
+        if (!beside) wait_for_previous();
     };
     const float g = clamp_log_gate(p.decay[h]);
     if (tid <= C) m->pw[tid] = expf(g * (float)tid);
@@ -301,7 +303,6 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         float2 S[32];
         wait_here();
-        if (OUT && !p.late) launch_dependents();
         // the state that enters: between segments, the caller's, or zero
         const float *from = OUT && seg.index > 0 ? p.seg + ((size_t)(seg.state - 1) * p.H + h) * (D * D)
                             : seg.index > 0 || p.s_in == nullptr ? nullptr : p.s_in + state_at;
@@ -425,7 +426,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             if (OUT && b + 1 < blocks) split_v(b + 1);
         }
         // an earlier pass of this call may still read the states, or run beside this one
-        if (!OUT || p.late) wait_for_previous();
+        if (beside) wait_for_previous();
         if (want_state) {
             float4 *dst = reinterpret_cast<float4 *>((OUT ? p.s_out + state_at : seg_out) + r * D + half * 64);
 #pragma unroll
