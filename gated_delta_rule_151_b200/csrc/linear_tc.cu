@@ -14,14 +14,14 @@
 // value channels on the TMEM lanes, so neither wastes half of the unit on 64
 // tokens, and S can be its own A operand from TMEM.
 //
-// Rounding.  A, B, V are exact bf16 operands.  P and the copy of S that meets A
-// are rounded to bf16: over many outputs that adds at most about one output
-// rounding to o, in quadrature.  A few outputs of a few tokens may each hang on one
-// score, whose rounding nothing averages out; there (kTwoPartOutputs) P enters
-// its product as two bf16 terms.  The state itself is never rounded: it stays in
-// fp32 registers, and diag(w) V enters its product as three bf16 terms (24
-// significant bits), so S is as exact as fp32 sums make it over any number of
-// blocks.
+// Rounding.  A, B, V are exact bf16 operands.  P and the copy of S that meets A enter
+// their products as two bf16 terms each (16 significant bits), so that a result has the
+// one rounding of its own type: with one term each it was 1.4 output roundings off, and
+// more where a few tokens hang on one score.  (The second terms take 15 %: 1 x 8192
+// tokens, 16 heads 52 -> 60 us of GPU time, the gradient 177 -> 217; half of it the
+// packing of S, a tenth the products.)  The state itself is never rounded: it stays
+// in fp32 registers, and diag(w) V enters its product as three bf16 terms (24 significant
+// bits), so S is as exact as fp32 sums make it over any number of blocks.
 //
 // 16 warps: 0-1 turn the scores into P (one row a thread); 2 issues the products
 // of a block's tokens alone (scores, (diag(w) V)^T B), 3 starts the TMA loads into
@@ -51,10 +51,12 @@ struct Shape {
     static constexpr uint32_t V_OFF = B_OFF + TILE;
     static constexpr uint32_t P_OFF = NS * STAGE;            // two buffers of 64 x 64 bf16, high and low part
     static constexpr uint32_t O_OFF = P_OFF + (OUT ? 2 * 16384 : 0);  // a tile of O on its way out
-    static constexpr uint32_t MISC = O_OFF + (OUT ? TILE : 0);
-    // TMEM columns
+    static constexpr uint32_t W_OFF = O_OFF + (OUT ? TILE : 0);      // the low part of diag(w) V, laid out as V
+    static constexpr uint32_t MISC = W_OFF + (OUT ? TILE : 0);
+    // TMEM columns.  Beside the two copies of S there is no room for the low part of the split V.
+    static constexpr uint32_t W_COLS = OUT ? 64 : 96;
     static constexpr uint32_t T_KV = 0;                      // NB of 128: (diag(w) V)^T B
-    static constexpr uint32_t T_W = NB * 128;                // NB of 96: (diag(w) V)^T, its high, middle, low part
+    static constexpr uint32_t T_W = NB * 128;                // NB of W_COLS: (diag(w) V)^T, its high, middle (low) part
 };
 
 struct Misc {
@@ -62,8 +64,8 @@ struct Misc {
     uint64_t w_full[4];                 // half of the split V is written
     uint64_t kv_full[4], kv_free[2];    // its product is done (and its buffer free), and read
     uint64_t sc_full[2], p_full[2];     // scores are done; P is written
-    uint64_t s_full;                    // S in bf16 is written
-    uint64_t done[3], o_free[2];        // S A^T and V^T P^T are done; they are read
+    uint64_t s_full, s_free;            // S in bf16 is written; S A^T is done
+    uint64_t done[3], o_free[2];        // V^T P^T is done too; they are read
     uint64_t end[2];
     uint32_t tmem;
     int abort;
@@ -78,6 +80,7 @@ template <bool OUT>
 constexpr int smem_bytes() { return (int)(Shape<OUT>::MISC + sizeof(Misc)); }
 static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "shared memory");
 
+constexpr uint32_t T_SL = 192;      // what S in bf16 leaves, in bf16
 constexpr uint32_t T_X = 256;       // two buffers of 64: a block's scores, then its V^T P^T
 constexpr uint32_t T_OI = 384;      // S A^T
 constexpr uint32_t T_SB = 448;      // S in bf16
@@ -86,12 +89,7 @@ constexpr uint32_t T_COLS = 512;
 constexpr uint32_t ID_N64 = make_idesc(1, 128, 64);
 constexpr uint32_t ID_PV = ID_N64 | kIdescAMN;
 constexpr uint32_t ID_KV = make_idesc(1, 128, 128) | kIdescBMN;
-
-// Up to this many outputs of d_v values P has two parts.  The second one costs the
-// long passes 15 % (1 x 8192 tokens, 16 heads: 61 to 65 us; its gradient 152 to 178),
-// short ones nothing (77 tokens: 17 us either way); one part leaves the result 1.4
-// output roundings off where outputs are many, and up to 2.6 where one score decides.
-constexpr int64_t kTwoPartOutputs = 4096;
+static_assert(Shape<true>::T_W + Shape<true>::W_COLS <= T_SL && T_SL + 64 <= T_X, "TMEM columns");
 
 enum : uint32_t { E_ALIGN = 1, E_TMA = 2, E_MMA = 4, E_HANDOFF = 8 };
 
@@ -184,8 +182,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+// What a pair's bf16 values leave of it, in bf16.
+__device__ __forceinline__ uint32_t rest_bf16(float2 f, uint32_t x) {
+    const float2 r = __ffma2_rn(make_float2(bf16_lo(x), bf16_hi(x)), make_float2(-1.f, -1.f), f);
+    return pack_bf16(r.x, r.y);
+}
 
-template <bool OUT, bool REV, typename OutT, bool TWO>
+template <bool OUT, bool REV, typename OutT>
 __global__ void __launch_bounds__(kThreads, 1)
 scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                const __grid_constant__ CUtensorMap mv, const ScanArgs p) {
@@ -254,6 +257,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                 mbar_init(&m->o_free[b], kOThreads);
             }
             mbar_init(&m->s_full, kSThreads);
+            mbar_init(&m->s_free, 1);
             mbar_init(&m->end[0], 1);
             mbar_init(&m->end[1], 1);
             m->abort = 0;
@@ -323,12 +327,18 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             }
         }
         bool ok = true;
+        // where a lane's row of eight channels lies, in V's tile: 16 tokens from 32 h2 + 16 k
+        auto v_at = [&](int ch, int h2, int k) {
+            const int j = h2 * 32 + k * 16 + (lane & 7) + ((lane >> 4) << 3);
+            return (uint32_t)((ch >> 6) * 8192) + sw128_offset(j, (ch >> 3) & 7);
+        };
         // (diag(w) V)^T of block b in three bf16 parts to TMEM, the product's other operand:
         // 32 tokens, then the other 32, whose split the first ones' product hides.  A warp
         // takes 16 channels (half of its lanes) by the 32 tokens.  ldmatrix hands a thread
         // tokens 8 m + 2 (lane % 4) and the next one of channels lane / 4 + {0, 8}, the
         // fragment that tcgen05.st writes; through shared memory the parts cost 96 KB of its
-        // 336 KB of traffic a block, which was the bound.
+        // 336 KB of traffic a block, which was the bound.  The output pass leaves the low part
+        // there, as its TMEM holds the second copy of S.
         auto split_v = [&](int b) {
             const int s = b % Sh::NS, n = block_n(b);
             if (!(ok = warp_wait(BAR(full, s), b / Sh::NS, E_TMA))) return;
@@ -345,18 +355,18 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             }
             // (the product that last read this buffer was waited for by its update of S)
             tc_fence_after();
-#pragma unroll
+            // (rolled, as the instructions of all roles together are what the cache holds:
+            // unrolled, packed prompts took 170 us in place of 158)
+#pragma unroll 1
             for (int h2 = 0; h2 < 2; ++h2) {
                 if (b + 1 < blocks || want_state) {
                     const int ch = (warp & 3) * 32 + half * 16 + (lane & 8), j0 = h2 * 32 + 2 * (lane & 3);
                     uint32_t hi[8], mid[8], lo[8];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {      // 16 tokens
-                        const int j = h2 * 32 + k * 16 + (lane & 7) + ((lane >> 4) << 3);
-                        const uint32_t at = stage + Sh::V_OFF + (ch >> 6) * 8192 + sw128_offset(j, (ch >> 3) & 7);
                         asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(hi[4 * k]), "=r"(hi[4 * k + 1]), "=r"(hi[4 * k + 2]), "=r"(hi[4 * k + 3])
-                                     : "r"(at)
+                                     : "r"(stage + Sh::V_OFF + v_at(ch, h2, k))
                                      : "memory");
                     }
                     float2 weight[4];
@@ -380,10 +390,20 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                         f = __ffma2_rn(make_float2(bf16_lo(mid[e]), bf16_hi(mid[e])), minus, f);
                         lo[e] = pack_bf16(f.x, f.y);
                     }
-                    const uint32_t to = tmem + lanes + ((uint32_t)half << 20) + Sh::T_W + (b % Sh::NB) * 96 + h2 * 16;
+                    const uint32_t to = tmem + lanes + ((uint32_t)half << 20) + Sh::T_W + (b % Sh::NB) * Sh::W_COLS + h2 * 16;
                     tmem_st_frag(to, hi);
                     tmem_st_frag(to + 32, mid);
-                    tmem_st_frag(to + 64, lo);
+                    if (OUT) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::
+                                             "r"(sbase + Sh::W_OFF + v_at(ch, h2, k)),
+                                         "r"(lo[4 * k]), "r"(lo[4 * k + 1]), "r"(lo[4 * k + 2]), "r"(lo[4 * k + 3])
+                                         : "memory");
+                        if (h2 == 1) fence_proxy_async();
+                    } else {
+                        tmem_st_frag(to + 64, lo);
+                    }
                     tmem_wait_st();
                     tc_fence_before();
                 }
@@ -393,12 +413,15 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         if (blocks > 0) split_v(0);
         for (int b = 0; b < blocks && ok; ++b) {
             if (OUT) {
-                if (b > 0 && !(ok = warp_wait(BAR(done, (b - 1) % 3), (b - 1) / 3, E_MMA))) break;
+                if (b > 0 && !(ok = warp_wait(BAR(s_free, 0), b - 1, E_MMA))) break;
                 tc_fence_after();
                 uint32_t x[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = pack_bf16(S[i].x, S[i].y);
                 tmem_st32(tmem + lanes + T_SB + half * 32, x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = rest_bf16(S[i], x[i]);
+                tmem_st32(tmem + lanes + T_SL + half * 32, x);
                 tmem_wait_st();
                 tc_fence_before();
                 arrive(BAR(s_full, 0));
@@ -542,17 +565,23 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             const bool kv = b + 1 < blocks || want_state;
             if (kv && b >= Sh::NB && !(ok = warp_wait(BAR(kv_free, w), b / Sh::NB - 1, E_HANDOFF))) break;
             const uint64_t bd = mnmajor + (((b % Sh::NS) * Sh::STAGE + Sh::B_OFF) >> 4);
-            const uint32_t d = tmem + Sh::T_KV + w * D, a = tmem + Sh::T_W + w * 96;
+            const uint64_t lo = mnmajor + (Sh::W_OFF >> 4);
+            const uint32_t d = tmem + Sh::T_KV + w * D, a = tmem + Sh::T_W + w * Sh::W_COLS;
 #pragma unroll
             for (int h2 = 0; h2 < 2; ++h2) {
                 if (ok) ok = warp_wait(BAR(w_full, w * 2 + h2), b / Sh::NB, E_HANDOFF);
                 tc_fence_after();
                 if (ok && kv && elect_one()) {
 #pragma unroll
-                    for (int part = 2; part >= 0; --part)     // the small terms first
+                    for (int part = OUT ? 1 : 2; part >= 0; --part)     // the small terms first
 #pragma unroll
                         for (int k = 2 * h2; k < 2 * h2 + 2; ++k)
-                            mma_f16_ts(d, a + part * 32 + k * 8, bd + ((k * 2048) >> 4), ID_KV, part != 2 || k != 0);
+                            mma_f16_ts(d, a + part * 32 + k * 8, bd + ((k * 2048) >> 4), ID_KV, part != (OUT ? 1 : 2) || k != 0);
+                    if (OUT && h2 == 1) {     // (the low part is complete with the second half)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16_ss(d, lo + ((k * 2048) >> 4), bd + ((k * 2048) >> 4), ID_KV | kIdescAMN, 1);
+                    }
                     if (h2 == 1) mma_commit(&m->kv_full[b & 3]);
                 }
                 __syncwarp();
@@ -586,20 +615,23 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             const uint64_t pd = kmajor + ((Sh::P_OFF + (b & 1) * 16384) >> 4);
             if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_f16_ts(tmem + T_OI, tmem + T_SB + k * 8, ad + (((k >> 2) * 8192 + (k & 3) * 32) >> 4),
-                               ID_N64, k != 0);
+                for (int part = 1; part >= 0; --part)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_f16_ts(tmem + T_OI, tmem + (part ? T_SL : T_SB) + k * 8,
+                                   ad + (((k >> 2) * 8192 + (k & 3) * 32) >> 4), ID_N64, part != 1 || k != 0);
+                mma_commit(&m->s_free);
             }
             __syncwarp();
             if (!warp_wait(BAR(p_full, b & 1), b >> 1, E_HANDOFF)) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int part = TWO; part >= 0; --part)
+                for (int part = 1; part >= 0; --part)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mma_f16_ss(tmem + T_X + (b & 1) * 64, vd + ((k * 2048) >> 4),
-                                   pd + ((part * 8192 + k * 32) >> 4), ID_PV, part != TWO || k != 0);
+                                   pd + ((part * 8192 + k * 32) >> 4), ID_PV, part != 1 || k != 0);
                 mma_commit(&m->done[b % 3]);
             }
             __syncwarp();
@@ -621,61 +653,51 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         // ------------------------------------------- P = scores .* decay, row i ----
         const int i = tid;
         const uint32_t lanes = (uint32_t)warp << 21;
-        float2 decay[32];            // row i of M
+        // Row i of M in halves of 32 columns: one lies on the diagonal, the other one on the
+        // causal side of all of this warp's rows or on the other side of them all.
+        float2 near[16], far[16];
 #pragma unroll
-        for (int j = 0; j < C; j += 2) {
-            const int a0 = REV ? j - i : i - j, a1 = REV ? j + 1 - i : i - j - 1;
-            decay[j / 2] = make_float2(a0 >= 0 ? m->pw[max(a0, 0)] : 0.f, a1 >= 0 ? m->pw[max(a1, 0)] : 0.f);
+        for (int e = 0; e < 32; e += 2) {
+            const int a0 = REV ? e - lane : lane - e, a1 = REV ? a0 + 1 : a0 - 1;
+            near[e / 2] = make_float2(m->pw[max(a0, 0)], m->pw[max(a1, 0)]);
+            far[e / 2] = make_float2(m->pw[32 + a0], m->pw[32 + a1]);
         }
+        const bool both = warp == (REV ? 0 : 1);
+        if (!both)                       // zeros that stay
+            for (int q = 0; q < 16; ++q)
+                st_shared_v4(sbase + Sh::P_OFF + (q >> 2) * 8192 + sw128_offset(i, (1 - warp) * 4 + (q & 3)), 0, 0, 0, 0);
         for (int b = 0; b < blocks; ++b) {
             if (b == 1) wait_here();
             if (!warp_wait(BAR(sc_full, b & 1), b >> 1, E_MMA)) break;
             if (b >= 2 && !warp_wait(BAR(done, (b - 2) % 3), (b - 2) / 3, E_MMA)) break;
             tc_fence_after();
-            const int n = block_n(b);
-            const uint32_t dst = sbase + Sh::P_OFF + (b & 1) * 16384;
-            // 32 columns at a time: they lie on the diagonal of this warp's rows, all on their
-            // causal side, or all on the other
-            auto columns = [&](auto which) {
-                constexpr int half = decltype(which)::value;
-                const uint32_t at = tmem + lanes + T_X + (b & 1) * 64 + half * 32;
+            const uint32_t dst = sbase + Sh::P_OFF + (b & 1) * 16384, from = tmem + lanes + T_X + (b & 1) * 64;
+            auto columns = [&](auto on_diagonal, const float2 (&decay)[16], int half) {
                 uint32_t x[32];
-                auto parts = [&](float2 s, uint32_t &hi, uint32_t &lo) {
-                    hi = pack_bf16(s.x, s.y);
-                    lo = TWO ? pack_bf16(s.x - bf16_lo(hi), s.y - bf16_hi(hi)) : 0;
-                };
-                uint32_t hi[16], lo[16];
-                if (half == warp || (REV && n < C)) {
-                    tmem_ld32(at, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {    // masked by selection: a score may be anything there
-                        const int j = half * 32 + e;
-                        float2 s = __fmul2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), decay[j / 2]);
-                        s.x = (REV ? j >= i && j < n : j <= i) ? s.x : 0.f;
-                        s.y = (REV ? j + 1 >= i && j + 1 < n : j + 1 <= i) ? s.y : 0.f;
-                        parts(s, hi[e / 2], lo[e / 2]);
-                    }
-                } else if (REV ? half < warp : half > warp) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0;
-                } else {
-                    tmem_ld32(at, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        parts(__fmul2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), decay[(half * 32 + e) / 2]),
-                              hi[e / 2], lo[e / 2]);
-                }
+                tmem_ld32(from + half * 32, x);
+                tmem_wait_ld();
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int e = q * 8 + u * 2;
+                        float2 s = __fmul2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), decay[e / 2]);
+                        if (decltype(on_diagonal)::value) {    // by selection: a score may be anything there
+                            s.x = (REV ? e >= lane : e <= lane) ? s.x : 0.f;
+                            s.y = (REV ? e + 1 >= lane : e + 1 <= lane) ? s.y : 0.f;
+                        }
+                        hi[u] = pack_bf16(s.x, s.y);
+                        lo[u] = rest_bf16(s, hi[u]);
+                    }
                     const uint32_t to = dst + sw128_offset(i, half * 4 + q);
-                    st_shared_v4(to, hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-                    if (TWO) st_shared_v4(to + 8192, lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+                    st_shared_v4(to, hi[0], hi[1], hi[2], hi[3]);
+                    st_shared_v4(to + 8192, lo[0], lo[1], lo[2], lo[3]);
                 }
             };
-            columns(std::integral_constant<int, 0>{});
-            columns(std::integral_constant<int, 1>{});
+            // (behind a reversed segment's last token the scores are zeros, as B's rows are)
+            columns(std::true_type{}, near, warp);
+            if (both) columns(std::false_type{}, far, 1 - warp);
             tc_fence_before();
             fence_proxy_async();
             arrive(BAR(p_full, b & 1));
@@ -690,21 +712,14 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
     }
 }
 
-template <bool OUT, bool REV, typename OutT, bool TWO>
+template <bool OUT, bool REV, typename OutT>
 cudaError_t launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mv,
                    const ScanArgs &p, bool after, cudaStream_t stream) {
-    auto fn = scan_tc_kernel<OUT, REV, OutT, TWO>;
+    auto fn = scan_tc_kernel<OUT, REV, OutT>;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(fn), smem_bytes<OUT>());
     if (e != cudaSuccess) return e;
     return launch_kernel(after, fn, dim3((unsigned)(OUT ? p.slots : p.inner) * p.H), kThreads, smem_bytes<OUT>(),
                          stream, ma, mb, mv, p);
-}
-
-template <bool REV, typename OutT>
-cudaError_t launch_out(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mv,
-                       const ScanArgs &p, bool after, cudaStream_t stream) {
-    return (int64_t)p.total_T * p.H <= kTwoPartOutputs ? launch<true, REV, OutT, true>(ma, mb, mv, p, after, stream)
-                                                       : launch<true, REV, OutT, false>(ma, mb, mv, p, after, stream);
 }
 
 }  // namespace
@@ -726,13 +741,13 @@ bool scan_tile_map(CUtensorMap *map, const void *base, int total_T, int H) {
 cudaError_t launch_scan_tc(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mv, const ScanArgs &p,
                            bool reverse, bool states, bool out_f32, bool after, cudaStream_t stream) {
     if (states)
-        return reverse ? launch<false, true, float, false>(ma, mb, mv, p, after, stream)
-                       : launch<false, false, float, false>(ma, mb, mv, p, after, stream);
+        return reverse ? launch<false, true, float>(ma, mb, mv, p, after, stream)
+                       : launch<false, false, float>(ma, mb, mv, p, after, stream);
     if (out_f32)
-        return reverse ? launch_out<true, float>(ma, mb, mv, p, after, stream)
-                       : launch_out<false, float>(ma, mb, mv, p, after, stream);
-    return reverse ? launch_out<true, __nv_bfloat16>(ma, mb, mv, p, after, stream)
-                   : launch_out<false, __nv_bfloat16>(ma, mb, mv, p, after, stream);
+        return reverse ? launch<true, true, float>(ma, mb, mv, p, after, stream)
+                       : launch<true, false, float>(ma, mb, mv, p, after, stream);
+    return reverse ? launch<true, true, __nv_bfloat16>(ma, mb, mv, p, after, stream)
+                   : launch<true, false, __nv_bfloat16>(ma, mb, mv, p, after, stream);
 }
 
 }  // namespace gdr
