@@ -73,6 +73,9 @@ struct Misc {
     float pw[kScanBlock + 1];                // x^k
     alignas(16) float lead[kScanBlock];      // of S A^T in a full block
     alignas(16) float weight[kScanBlock];    // of V in a full block
+    // Of four blocks in turn: the last one whose V had infinities or NaN, in any of its
+    // channels and in 16 of them each, and its first (reverse: last) such token per channel.
+    int bad[4], bad_part[4][8], bad_token[4][128];
 };
 
 static_assert(Shape<true>::NS == 3 && Shape<false>::NS == 4, "copies of done and kv_full");
@@ -188,6 +191,38 @@ __device__ __forceinline__ uint32_t rest_bf16(float2 f, uint32_t x) {
     return pack_bf16(r.x, r.y);
 }
 
+// Infinities and NaN of V, which the zeros of P would carry to tokens on the other side of
+// the mask: they leave the tile, and the tokens that they do reach get NaN where O is
+// written (the split V has them, and so has S).  A warp looks through its 16 channels of the
+// block's tokens.  Both are rare, and kept out of line.
+template <bool REV>
+__device__ __noinline__ void take_out(uint32_t v, int n, int b, Misc *m) {
+    const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) & 7;
+    const int c = (part & 3) * 32 + (part >> 2) * 16 + (lane & 15);
+    int found = REV ? -1 : C;
+    for (int j = lane >> 4; j < n; j += 2) {
+        const uint32_t at = v + (c >> 6) * 8192 + sw128_offset(j, (c >> 3) & 7) + (c & 7) * 2;
+        uint16_t x;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at) : "memory");
+        if ((x & 0x7f80) != 0x7f80) continue;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)0) : "memory");
+        found = REV ? j : min(found, j);
+    }
+    const int other = __shfl_xor_sync(0xffffffffu, found, 16);
+    m->bad_token[b & 3][c] = REV ? max(found, other) : min(found, other);
+    m->bad_part[b & 3][part] = b;
+    m->bad[b & 3] = b;
+    fence_proxy_async();
+}
+
+// NaN to the tokens of channel c that it reaches: `put` of each.
+template <bool REV, typename Put>
+__device__ __noinline__ void put_back(int c, int n, int b, const Misc *m, Put put) {
+    if (m->bad_part[b & 3][(c >> 5) + ((c >> 4) & 1) * 4] != b) return;
+    const int token = m->bad_token[b & 3][c];
+    for (int i = REV ? 0 : token; i < (REV ? token + 1 : n); ++i) put(i);
+}
+
 template <bool OUT, bool REV, typename OutT>
 __global__ void __launch_bounds__(kThreads, 1)
 scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
@@ -280,6 +315,10 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
         m->lead[tid] = expf(g * (float)(REV ? C - 1 - tid : tid + 1));
         m->weight[tid] = expf(g * (float)(REV ? tid + 1 : C - 1 - tid));
     }
+    if (OUT && tid < 32) {
+        m->bad[tid & 3] = -1;
+        m->bad_part[tid >> 3][tid & 7] = -1;
+    }
     if (warp == 0) {
         tmem_alloc(&m->tmem, T_COLS);
         tmem_relinquish();
@@ -355,11 +394,13 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             }
             // (the product that last read this buffer was waited for by its update of S)
             tc_fence_after();
+            __nv_bfloat162 any = __float2bfloat162_rn(0.f);
             // (rolled, as the instructions of all roles together are what the cache holds:
             // unrolled, packed prompts took 170 us in place of 158)
 #pragma unroll 1
             for (int h2 = 0; h2 < 2; ++h2) {
-                if (b + 1 < blocks || want_state) {
+                const bool kv = b + 1 < blocks || want_state;
+                if (OUT || kv) {
                     const int ch = (warp & 3) * 32 + half * 16 + (lane & 8), j0 = h2 * 32 + 2 * (lane & 3);
                     uint32_t hi[8], mid[8], lo[8];
 #pragma unroll
@@ -369,46 +410,61 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                                      : "r"(stage + Sh::V_OFF + v_at(ch, h2, k))
                                      : "memory");
                     }
-                    float2 weight[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) weight[k] = *reinterpret_cast<const float2 *>(m->weight + j0 + 8 * k);
                     if (n < C) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const int j = j0 + 8 * (e >> 1);
                             hi[e] = j + 1 < n ? hi[e] : j < n ? hi[e] & 0xffffu : 0u;
-                            if (!REV) weight[e >> 1] = make_float2(m->pw[max(n - 1 - j, 0)], m->pw[max(n - 2 - j, 0)]);
                         }
                     }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float2 minus = make_float2(-1.f, -1.f);
-                        float2 f = __fmul2_rn(make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])), weight[e >> 1]);
-                        hi[e] = pack_bf16(f.x, f.y);
-                        f = __ffma2_rn(make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])), minus, f);
-                        mid[e] = pack_bf16(f.x, f.y);
-                        f = __ffma2_rn(make_float2(bf16_lo(mid[e]), bf16_hi(mid[e])), minus, f);
-                        lo[e] = pack_bf16(f.x, f.y);
-                    }
-                    const uint32_t to = tmem + lanes + ((uint32_t)half << 20) + Sh::T_W + (b % Sh::NB) * Sh::W_COLS + h2 * 16;
-                    tmem_st_frag(to, hi);
-                    tmem_st_frag(to + 32, mid);
                     if (OUT) {
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::
-                                             "r"(sbase + Sh::W_OFF + v_at(ch, h2, k)),
-                                         "r"(lo[4 * k]), "r"(lo[4 * k + 1]), "r"(lo[4 * k + 2]), "r"(lo[4 * k + 3])
-                                         : "memory");
-                        if (h2 == 1) fence_proxy_async();
-                    } else {
-                        tmem_st_frag(to + 64, lo);
+                        for (int e = 0; e < 8; ++e)      // NaN if one of them is not finite, else 0
+                            any = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&hi[e]), __float2bfloat162_rn(0.f), any);
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
+                    if (kv) {
+                        float2 weight[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) weight[k] = *reinterpret_cast<const float2 *>(m->weight + j0 + 8 * k);
+                        if (!REV && n < C) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int j = j0 + 8 * k;
+                                weight[k] = make_float2(m->pw[max(n - 1 - j, 0)], m->pw[max(n - 2 - j, 0)]);
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 minus = make_float2(-1.f, -1.f);
+                            float2 f = __fmul2_rn(make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])), weight[e >> 1]);
+                            hi[e] = pack_bf16(f.x, f.y);
+                            f = __ffma2_rn(make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])), minus, f);
+                            mid[e] = pack_bf16(f.x, f.y);
+                            f = __ffma2_rn(make_float2(bf16_lo(mid[e]), bf16_hi(mid[e])), minus, f);
+                            lo[e] = pack_bf16(f.x, f.y);
+                        }
+                        const uint32_t to = tmem + lanes + ((uint32_t)half << 20) + Sh::T_W + (b % Sh::NB) * Sh::W_COLS + h2 * 16;
+                        tmem_st_frag(to, hi);
+                        tmem_st_frag(to + 32, mid);
+                        if (OUT) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::
+                                                 "r"(sbase + Sh::W_OFF + v_at(ch, h2, k)),
+                                             "r"(lo[4 * k]), "r"(lo[4 * k + 1]), "r"(lo[4 * k + 2]), "r"(lo[4 * k + 3])
+                                             : "memory");
+                            if (h2 == 1) fence_proxy_async();
+                        } else {
+                            tmem_st_frag(to + 64, lo);
+                        }
+                        tmem_wait_st();
+                        tc_fence_before();
+                    }
                 }
                 arrive(BAR(w_full, (b % Sh::NB) * 2 + h2));
             }
+            if (OUT && __any_sync(0xffffffffu, (*reinterpret_cast<const uint32_t *>(&any) & 0x7fff7fffu) != 0))
+                take_out<REV>(stage + Sh::V_OFF, n, b, m);
         };
         if (blocks > 0) split_v(0);
         for (int b = 0; b < blocks && ok; ++b) {
@@ -524,14 +580,25 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
                     }
                 }
             }
+            const bool bad = m->bad[b & 3] == b;
             if constexpr (sizeof(OutT) == 2) {
                 if (group_stop(1, kOThreads, false)) break;
+                if (bad) {
+                    put_back<REV>(t, n, b, m, [=](int i) {
+                        const uint32_t at = sbase + Sh::O_OFF + i * 256 + (((t >> 3) ^ (i & 7)) << 4) + (t & 7) * 2;
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)0x7fff) : "memory");
+                    });
+                    if (group_stop(1, kOThreads, false)) break;
+                }
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const int e = u * kOThreads + t, i = e >> 4, piece = e & 15;
                     const uint4 x = *reinterpret_cast<const uint4 *>(sm + Sh::O_OFF + i * 256 + ((piece ^ (i & 7)) << 4));
                     if (i < n) *reinterpret_cast<uint4 *>(dst + i * row + piece * 8) = x;
                 }
+            } else if (bad) {
+                if (group_stop(1, kOThreads, false)) break;     // (the tile is written)
+                put_back<REV>(t, n, b, m, [=](int i) { store_io(dst + i * row + t, __uint_as_float(0x7fffffffu)); });
             }
         }
     } else if (warp == 2) {

@@ -469,9 +469,10 @@ GDR_API gdr_status_t gdr_backward(const void *q, const void *k, const void *v, c
  * bf16 with d_k = d_v = 128 runs on the tensor cores: 64-token blocks, the
  * scores and the copy of the state that meets the queries in two bf16 terms
  * each (16 significant bits), the state itself fp32 throughout.  Other shapes
- * and fp32 run in fp32 on the CUDA cores.  Infinities and NaN stay inside their
- * (sequence, head); a non-finite value in v or k leaves NaN in every later
- * output it reaches.
+ * and fp32 run in fp32 on the CUDA cores.  An infinity or NaN makes the results
+ * that depend on it infinite or NaN and leaves all others as they were: one in
+ * v, k or the incoming state reaches its own token's and later outputs of its
+ * (sequence, head), one in q its own token's alone.
  *
  * cu_seqlens, initial_state, final_state (which may be initial_state) and
  * empty sequences as for gdr_prefill_chunked; cu_seqlens needs 4-byte
