@@ -641,7 +641,9 @@ def _linear_args(q, k, v, decay, cu_seqlens, num_seqs):
         if num_seqs is not None and int(num_seqs) != N:
             raise ValueError(f"num_seqs is {num_seqs}, cu_seqlens has {N} sequences")
     else:
-        N = 1 if num_seqs is None else _int32(int(num_seqs), "num_seqs")
+        N = 1 if num_seqs is None else int(num_seqs)
+    if max(T, Hqk, H, dk, dv, abs(N)) >= 1 << 31:      # (ctypes would cut them to 32 bits)
+        raise ValueError(f"sizes must fit 32 bits, got T {T}, heads {Hqk} and {H}, d {dk} and {dv}, {N} sequences")
     return T, Hqk, H, dk, dv, N, dev, io
 
 

@@ -142,3 +142,16 @@ def test_binding_refuses_sizes_beyond_32_bits(size):
     assert size(0) >= 0
     with pytest.raises(ValueError):
         size(1 << 32)
+
+
+@pytest.mark.parametrize("sizes", [dict(N=1 << 32), dict(T=1 << 32), dict(H=1 << 32), dict(d=1 << 32), dict(num_seqs=(1 << 32) + 1)],
+                         ids=lambda s: next(iter(s)))
+def test_tensors_beyond_32_bits_are_refused(sizes, monkeypatch):
+    """Tensors without storage whose sizes, cut to 32 bits, are those of a good call."""
+    monkeypatch.setattr(gdr, "_need", lambda *a, **kw: None)
+    s = dict(N=0, T=0, H=0, d=0, num_seqs=None) | sizes
+    new = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device="meta")  # noqa: E731
+    q, v = new(64 + s["T"], 2, 16 + s["d"]), new(64 + s["T"], 2 + s["H"], 16)
+    cu = None if s["num_seqs"] else new(2 + s["N"], dtype=torch.int32)
+    with pytest.raises(ValueError, match="32 bits"):
+        gdr._linear_args(q, q, v, new(2 + s["H"]), cu, s["num_seqs"])
