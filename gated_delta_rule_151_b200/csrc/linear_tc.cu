@@ -625,8 +625,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             }
             __syncwarp();
         };
+        // (here and below: the polls that follow do not count that time; those of a first block
+        // that is not full wait for the split of V, and with it for the states)
+        if (block_n(0) < C) wait_here();
         if (OUT && blocks > 0) scores(0);
-        wait_here();   // (here and below: the polls that follow do not count that time)
+        wait_here();
         for (int b = 0; b < blocks && ok; ++b) {
             const int w = b % Sh::NB;
             const bool kv = b + 1 < blocks || want_state;
@@ -734,7 +737,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ C
             for (int q = 0; q < 16; ++q)
                 st_shared_v4(sbase + Sh::P_OFF + (q >> 2) * 8192 + sw128_offset(i, (1 - warp) * 4 + (q & 3)), 0, 0, 0, 0);
         for (int b = 0; b < blocks; ++b) {
-            if (b == 1) wait_here();
+            if (b == (block_n(0) == C)) wait_here();
             if (!warp_wait(BAR(sc_full, b & 1), b >> 1, E_MMA)) break;
             if (b >= 2 && !warp_wait(BAR(done, (b - 2) % 3), (b - 2) / 3, E_MMA)) break;
             tc_fence_after();
