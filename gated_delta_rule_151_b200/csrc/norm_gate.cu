@@ -68,9 +68,11 @@ __device__ __forceinline__ void put2(float *f, float2 x) { f[0] = x.x; f[1] = x.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
-// Single-instruction exponential and reciprocal: together within 2^-21 (1 + |z| / 8) of
-// the value.  The full-precision pair took the heads' forward pass from 23 to 35 us.
-__device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.0f + ex2_approx(-kLog2e * z)); }
+// e^-z, and with it the sigmoid 1 / (1 + e^-z).  For bf16 tensors the single-instruction
+// exponential, within 2^-20 (1 + |z| / 8) of the value, where the result's rounding is 2^-8;
+// the full-precision one takes the heads' forward pass from 23 to 35 us.  fp32 tensors get it.
+template <int E>
+__device__ __forceinline__ float exp_minus(float z) { return E == 8 ? ex2_approx(-kLog2e * z) : expf(-z); }
 
 // act(z) in place of z and, for the gradient, act'(z), of a piece.  The choice stands
 // outside the channels' loops, whose exponentials then overlap.
@@ -80,7 +82,7 @@ __device__ __forceinline__ void act_of(int act, float (&z)[E]) {
     const bool silu = act == kActSilu;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const float s = sigmoid(z[e]);
+        const float s = rcp_approx(1.f + exp_minus<E>(z[e]));
         z[e] = s * (silu ? z[e] : 1.f);
     }
 }
@@ -94,7 +96,9 @@ __device__ __forceinline__ void act_both(int act, float (&z)[E], float (&da)[E])
     const bool silu = act == kActSilu;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const float s = sigmoid(z[e]), rest = 1.f - s;
+        // what the sigmoid leaves to 1, as a product: the difference has no bits left beyond
+        // z = 15 (and is 1 % off at 10 in bf16).  Where e^-z overflows s is 0.
+        const float x = exp_minus<E>(z[e]), s = rcp_approx(1.f + x), rest = s * fminf(x, 0x1p127f);
         da[e] = s * (silu ? fmaf(z[e], rest, 1.f) : rest);
         z[e] = s * (silu ? z[e] : 1.f);
     }
