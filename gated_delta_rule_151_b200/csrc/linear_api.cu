@@ -39,7 +39,7 @@ struct Costs {
 bool tensor_cores(int d_k, int d_v, bool bf16) { return bf16 && d_k == 128 && d_v == 128; }
 
 Costs costs_of(int d_k, int d_v, bool bf16) {
-    if (tensor_cores(d_k, d_v, bf16)) return Costs{true, 1.6, 1.6, 0.9, 0.9, 4.0, 5.0};
+    if (tensor_cores(d_k, d_v, bf16)) return Costs{true, 2.1, 2.1, 0.9, 0.9, 4.0, 5.0};
     const double x = (double)d_k * d_v / 16384;
     return Costs{false, 9 + 28 * x, 29 * x, 4 + 10 * x, 12 * x, 3.0, 4.0};
 }
