@@ -193,50 +193,50 @@ __device__ __forceinline__ void unit_lower_inverse(const float *Af, float *Tf, f
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static bool tried = false;
-    if (!tried) {
-        tried = true;
+// cuTensorMapEncodeTiled, looked up once; the threads that ask first wait for it.  It needs a
+// current context, which a thread has only after a runtime call that makes the device's its
+// own: a thread's first CUDA call may be this one.
+template <typename... Args>
+bool encode_map(Args... args) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                            cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+    }();
+    if (encode == nullptr) return false;
+    CUresult r = encode(args...);
+    int device;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess)
+        r = encode(args...);
+    return r == CUDA_SUCCESS;
 }
 
 // [total_T, H, 128] bf16 viewed as a 3-D tensor {128, H, total_T}; box
 // {64, 1, 64} with 128-byte swizzle: one 64-token x 64-channel tile.
 bool make_map(CUtensorMap *map, const void *base, int total_T, int H) {
-    auto enc = get_encode();
-    if (enc == nullptr) return false;
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)total_T};
     cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
     cuuint32_t box[3] = {64, 1, 64};
     cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
                      strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
 }
 
 // [total_T, H, 128] fp32 per-channel gates viewed as {128, H, total_T}; box
 // {32, 1, 64} without swizzle: 64 tokens x 32 channels as rows of 128 bytes.
 bool make_gate_map(CUtensorMap *map, const float *base, int total_T, int H) {
-    auto enc = get_encode();
-    if (enc == nullptr) return false;
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)total_T};
     cuuint64_t strides[2] = {(cuuint64_t)D * 4, (cuuint64_t)H * D * 4};
     cuuint32_t box[3] = {32, 1, 64};
     cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float *>(base), dims,
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float *>(base), dims,
                      strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
 }
 
 }  // namespace

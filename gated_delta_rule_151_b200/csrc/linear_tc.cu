@@ -797,15 +797,13 @@ cudaError_t launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorM
 // [T, H, 128] bf16 seen as {64 channels, T, 2 halves, H}: one box is a tile of 64
 // tokens by 128 channels of one head, its halves one after the other.
 bool scan_tile_map(CUtensorMap *map, const void *base, int total_T, int H) {
-    auto enc = get_encode();
-    if (enc == nullptr) return false;
     cuuint64_t dims[4] = {64, (cuuint64_t)total_T, 2, (cuuint64_t)H};
     cuuint64_t strides[3] = {(cuuint64_t)H * D * 2, 128, (cuuint64_t)D * 2};
     cuuint32_t box[4] = {64, C, 2, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 cudaError_t launch_scan_tc(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mv, const ScanArgs &p,

@@ -1,5 +1,9 @@
 """Linear attention with a decay for each head over lengths that are cut into segments and calls with many
 outputs, where the kernels' passes follow one another and every rounding counts."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -144,3 +148,37 @@ def test_bf16_results_do_not_depend_on_the_batch():
         alone, _ = gdr.gdr_linear_prefill(y["q"], y["k"], y["v"], y["decay"], y["state"])
         for a, b in zip((o, *grads[:3]), (alone, *backward(y)[:3])):
             assert (a[t].double() - b.double()).norm() <= 2.0 ** -11 * b.double().norm()
+
+
+FIRST_CALLS = """
+import sys, threading, torch
+from gated_delta_rule_151_b200 import gdr
+torch.manual_seed(0)
+n = int(sys.argv[1])
+q = torch.nn.functional.normalize(torch.randn(300, 2, 128, device="cuda"), dim=-1).bfloat16()
+v, decay, beta = torch.randn_like(q), torch.tensor([-0.1, -0.01], device="cuda"), torch.rand(300, 2, device="cuda")
+calls = [lambda: gdr.gdr_linear_prefill(q, q, v, decay), lambda: gdr.gdr_linear_backward(q, q, v, decay, d_o=v),
+         lambda: gdr.gdr_prefill_chunked(q, q, v, -beta, beta)]
+warm = [[torch.empty_like(v) for _ in range(64)], torch.empty(1 << 26, device="cuda")]
+del warm                     # (memory at hand: the threads' first CUDA call is the library's)
+torch.cuda.synchronize()
+for call in calls:
+    start, out = threading.Barrier(n), [None] * n
+    def run(i):
+        start.wait()
+        out[i] = call()
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(n)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert all(o is not None and all(torch.equal(a, b) for a, b in zip(o, call())) for o in out)
+"""
+
+
+@pytest.mark.parametrize("threads", [1, 16])
+def test_first_calls_of_threads(threads):
+    """The first calls of a process come from new threads, one or many at the same time: none finds the library
+    half set up or is refused for want of a context."""
+    run = subprocess.run([sys.executable, "-c", FIRST_CALLS, str(threads)], capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert run.returncode == 0, run.stderr[-2000:]
