@@ -142,7 +142,7 @@ struct Shape {
     static constexpr int ROWS = NT / TPR;                  // rows of a block at a time
     static constexpr int E = 16 / sizeof(T);
     // Row groups a block holds, one at work and the others on their way.  A third helps
-    // the gradient (8191 x 2048 fp32: 97 -> 86 us; a fourth nothing) and costs the forward
+    // the gradient (8191 x 2048 fp32: 97 -> 86 us of GPU time; a fourth nothing) and costs the forward
     // pass resident blocks (131,072 x 128 bf16: 18.7 -> 20.0 before the packed arithmetic).
     static constexpr int stages(bool back, int tensors) {
         return back && 3 * tensors * VPT * NT * 16 <= kMostRing ? 3 : 2;
@@ -151,9 +151,9 @@ struct Shape {
 
 // A thread's pieces of the next row groups, copied to shared memory without
 // registers while it works on this one.  Each thread reads only what it copied
-// itself: no barriers.  `Tensors` rows side by side.  Rows too wide for it (fp32
-// gradients beyond 4096 channels, every row beyond 8192) are read from memory where they
-// are used.
+// itself: no barriers.  `Tensors` rows side by side.  Two stages fit for rows of 16 KB with
+// any number of tensors and of 32 KB with up to three (all forward passes, gradients without
+// the second norm); wider ones are read from memory where they are used.
 template <typename T, int TPR, int VPT, int Tensors, int Stages>
 struct Ring {
     using Sh = Shape<T, TPR, VPT>;

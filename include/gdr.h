@@ -534,8 +534,10 @@ GDR_API gdr_status_t gdr_linear_check_workspace(const void *workspace, size_t wo
  * norm before the next.  weight NULL: x enters as it is.  gate NULL: no gate.
  * residual NULL: y = scale * u.  next_weight and y_norm go together and may be
  * NULL.  x, gate, residual, y, y_norm in the io dtype, weights fp32; the
- * arithmetic is fp32 and y_norm is taken from y before its rounding.  y may be
- * residual itself (updated in place); nothing else may overlap.
+ * arithmetic is fp32 and y_norm is taken from y before its rounding.  (A row
+ * whose sum of squares passes the range of fp32, elements beyond about 1e18,
+ * is normed to zeros.)  y may be residual itself (updated in place); nothing
+ * else may overlap.
  *
  * dim is a multiple of 8, at most 16384; eps > 0; all pointers 16-byte aligned.
  */
